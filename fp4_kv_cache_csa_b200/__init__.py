@@ -8,7 +8,8 @@ is no CPU fallback.
 
 The function names mirror the C ABI in include/csa.h:
     csa_compress_quantize, csa_index_topk, csa_decode_attend, hca_decode_attend,
-    csa_read_device_status (+ the workspace-size queries).
+    csa_read_device_status (+ the workspace-size queries),
+    csa_rotary, csa_rotary_frequencies.
 """
 from __future__ import annotations
 
@@ -27,6 +28,15 @@ CSA_IDX_MXFP4 = 2
 CSA_SCALE_E8M0_32 = 0  # one E8M0 scale byte per 32 elements (OCP MXFP4)
 CSA_SCALE_E4M3_16 = 1  # one E4M3 scale byte per 16 elements
 
+CSA_BF16 = 0
+CSA_F32 = 1
+CSA_ROPE_PAIRS = 0  # channels 2p, 2p + 1 turn together
+CSA_ROPE_HALF = 1   # channels p, p + rot_dim / 2 turn together
+CSA_ROPE_SCALE_NONE = 0
+CSA_ROPE_SCALE_LINEAR = 1
+CSA_ROPE_SCALE_BASE = 2
+CSA_ROPE_SCALE_PARTS = 3
+
 CSA_DEV_TOKEN_COUNT = 0x1
 CSA_DEV_CAPACITY = 0x2
 CSA_DEV_BAD_INDEX = 0x4
@@ -38,7 +48,7 @@ EXPORTED = (
     "csa_attend_workspace", "csa_decode_attend", "hca_decode_attend", "csa_read_device_status",
     "csa_index_topk_noalloc", "csa_index_pool_workspace", "csa_index_topk_pool", "csa_index_reindex_workspace",
     "csa_index_topk_reindex", "csa_index_reindex_layers_workspace", "csa_index_topk_reindex_layers",
-    "csa_probe_mxf4_mma",
+    "csa_probe_mxf4_mma", "csa_rotary", "csa_rotary_frequencies",
 )
 
 
@@ -54,6 +64,16 @@ class _CCache(ctypes.Structure):
         ("n_blocks", ctypes.c_void_p), ("status", ctypes.c_void_p), ("scale_fmt", ctypes.c_int32),
         ("idx_key_scale", ctypes.c_void_p),
     ]
+
+
+class _CVectors(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_begin", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("mscale", ctypes.c_float)]
 
 
 _lib = None
@@ -108,6 +128,11 @@ def declare(lib):
     lib.csa_read_device_status.restype = I
     lib.csa_probe_mxf4_mma.argtypes = [I, P, P, ctypes.POINTER(ctypes.c_int64)]
     lib.csa_probe_mxf4_mma.restype = I
+    VP, D = ctypes.POINTER(_CVectors), ctypes.c_double
+    lib.csa_rotary.argtypes = [VP, VP, I, I, I, ctypes.POINTER(_CRope), P, I, P]
+    lib.csa_rotary.restype = I
+    lib.csa_rotary_frequencies.argtypes = [I, D, I, D, I, D, D, P, P]
+    lib.csa_rotary_frequencies.restype = I
     return lib
 
 
@@ -127,6 +152,47 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream the call goes to: `stream`, or
+    that device's current one. Scratch made inside is kept alive for a stream that is not current."""
+
+    def __init__(self, device, stream):
+        import torch
+
+        self.guard = None
+        if device.type != "cuda":
+            raise CsaError(f"tensors must be on a CUDA device, not {device}")
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.device, self.given = device, stream
+
+    def __enter__(self):
+        import torch
+
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.stream = torch.cuda.current_stream() if self.given is None else self.given
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def scratch(self, t):
+        if self.given is not None:
+            t.record_stream(self.given)
+        return t
+
+
+def _expect(what, name, t, device, dtype, shape):
+    """One tensor of a call: on `device`, of `dtype`, dense, with this shape (None: any extent)."""
+    if t.device != device or t.dtype != dtype or not t.is_contiguous() or len(t.shape) != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = ", ".join("*" if n is None else str(n) for n in shape)
+        raise CsaError(f"{what}: {name} must be a dense {dtype} tensor [{want}] on {device}, not "
+                       f"{t.dtype} {list(t.shape)} on {t.device}")
 
 
 @dataclass
@@ -367,6 +433,58 @@ def hca_decode_attend(cache: Cache, q, q_offsets, q_pos, win_kv=None, win_start=
                                  _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)),
            "hca_decode_attend")
     return out
+
+
+def _vectors(what, name, t):
+    import torch
+
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise CsaError(f"{what}: {name} must be bfloat16 or float32, not {t.dtype}")
+    if t.dim() not in (2, 3) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise CsaError(f"{what}: {name} must be [rows, (heads,) dim] with adjacent channels")
+    return _CVectors(t.data_ptr(), CSA_BF16 if t.dtype == torch.bfloat16 else CSA_F32, t.stride(0),
+                     t.stride(1) if t.dim() == 3 else 0)
+
+
+def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layout: int = CSA_ROPE_PAIRS,
+               inverse: bool = False, mscale: float = 1.0, out_dtype=None, stream=None):
+    """Rotary positions: x [rows, (heads,) dim] bf16 or float32 (any strides, channels adjacent) with the
+    channels [rot_begin, rot_begin + 2 len(inv_freq)) turned by pos [rows] int32 * inv_freq float32
+    (rot_begin: the last ones by default). Returns `out`: x itself turns it in place; by default a new
+    tensor of out_dtype (x's type). inverse=True turns back, and is the gradient."""
+    import torch
+
+    lib, what = load_library(), "csa_rotary"
+    cx = _vectors(what, "x", x)
+    rows, dim = x.shape[0], x.shape[-1]
+    heads = x.shape[1] if x.dim() == 3 else 1
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or out.device != x.device or (out_dtype is not None and out.dtype != out_dtype):
+        raise CsaError(f"{what}: out must match x's shape and device, and out_dtype")
+    co = _vectors(what, "out", out)
+    _expect(what, "pos", pos, x.device, torch.int32, (rows,))
+    _expect(what, "inv_freq", inv_freq, x.device, torch.float32, (None,))
+    rot = 2 * inv_freq.shape[0]
+    rope = _CRope(inv_freq.data_ptr(), dim - rot if rot_begin is None else rot_begin, rot, layout, mscale)
+    with _On(x.device, stream) as s:
+        _check(lib.csa_rotary(ctypes.byref(cx), ctypes.byref(co), rows, heads, dim, ctypes.byref(rope),
+                              pos.data_ptr(), int(inverse), s), what)
+    return out
+
+
+def csa_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = CSA_ROPE_SCALE_NONE,
+                           factor: float = 1.0, original_len: int = 1, beta_fast: float = 32.0,
+                           beta_slow: float = 1.0):
+    """(inv_freq, mscale) for csa_rotary: float32 [rot_dim / 2] on the host, and the scale of its
+    outputs (1 but for CSA_ROPE_SCALE_PARTS). See include/csa.h for the scalings."""
+    import torch
+
+    inv = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32)
+    m = ctypes.c_float(1.0)
+    _check(load_library().csa_rotary_frequencies(rot_dim, base, scaling, factor, original_len, beta_fast, beta_slow,
+                                                 inv.data_ptr() or None, ctypes.byref(m)), "csa_rotary_frequencies")
+    return inv, float(m.value)
 
 
 def csa_probe_mxf4_mma(iters: int, status, stream=None) -> int:

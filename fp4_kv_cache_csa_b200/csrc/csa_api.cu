@@ -1,6 +1,7 @@
 // csa_api.cu -- the C ABI declared in include/csa.h: host-side argument checks,
 // workspace sizing and kernel dispatch. Nothing here allocates memory; every
 // call only enqueues work on the caller's stream.
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 
@@ -30,6 +31,8 @@ cudaError_t launch_attend(const csa_cache &c, const void *q, int Nq, int H, cons
                           const int32_t *q_pos, const int32_t *sel_idx, int topk, const void *win_kv,
                           const int64_t *win_start, const int32_t *win_len, int max_win, float softmax_scale,
                           float *out, float *lse, void *workspace, int num_ctas, cudaStream_t s);
+cudaError_t launch_rotary(const csa_vectors &x, const csa_vectors &out, int rows, int heads, int dim,
+                          const csa_rope &rope, const int32_t *pos, bool inverse, bool in_place, cudaStream_t s);
 }  // namespace csa
 
 namespace {
@@ -67,6 +70,67 @@ csa_status check_cache(const csa_cache *c) {
         }
     }
     return CSA_OK;
+}
+
+// ---- strided vectors (csa_rotary)
+constexpr int kMaxRotaryDim = 8192;
+
+struct VectorShape {
+    int64_t rows, heads, dim;
+};
+
+bool dtype_ok(int32_t t) { return t == CSA_BF16 || t == CSA_F32; }
+int dtype_size(int32_t t) { return t == CSA_BF16 ? 2 : 4; }
+
+// No negative strides, and no byte offset beyond 2^62 (nothing below can then wrap).
+bool strides_ok(const csa_vectors &v, const VectorShape &n) {
+    constexpr int64_t kMost = int64_t(1) << 60;
+    if (v.row_stride < 0 || v.head_stride < 0) return false;
+    if (n.rows > 1 && v.row_stride > kMost / n.rows) return false;
+    if (n.heads > 1 && v.head_stride > kMost / n.heads) return false;
+    return true;
+}
+int64_t row_step(const csa_vectors &v, const VectorShape &n) { return n.rows > 1 ? v.row_stride : 0; }
+int64_t head_step(const csa_vectors &v, const VectorShape &n) { return n.heads > 1 ? v.head_stride : 0; }
+
+bool same_layout(const csa_vectors &a, const csa_vectors &b, const VectorShape &n) {
+    return a.dtype == b.dtype && row_step(a, n) == row_step(b, n) && head_step(a, n) == head_step(b, n);
+}
+
+// Whether some offset row * rs + head * hs (not 0, 0 when `apart`) lies within dim of `delta`:
+// then two vectors share a channel. Checked over the axis with fewer steps.
+bool meets(int64_t delta, int64_t rs, int64_t hs, const VectorShape &n, bool apart) {
+    int64_t few = n.heads, many = n.rows, fs = hs, ms = rs;
+    if (n.rows < n.heads) {
+        few = n.rows, many = n.heads, fs = rs, ms = hs;
+    }
+    for (int64_t f = -(few - 1); f < few; ++f) {
+        const int64_t rest = delta - f * fs;  // look for m with |rest - m * ms| < dim, |m| < many
+        int64_t m = ms > 0 ? rest / ms : 0;
+        for (int64_t k = m - 1; k <= m + 1; ++k) {
+            if (k <= -many || k >= many || (apart && f == 0 && k == 0)) continue;
+            const int64_t d = rest - k * ms;
+            if (d < n.dim && -d < n.dim) return true;
+        }
+    }
+    return false;
+}
+bool self_overlap(const csa_vectors &v, const VectorShape &n) {
+    const int64_t rs = row_step(v, n), hs = head_step(v, n);
+    if ((n.heads == 1 || hs >= n.dim) && (n.rows == 1 || rs >= (n.heads - 1) * hs + n.dim)) return false;
+    return meets(0, row_step(v, n), head_step(v, n), n, true);
+}
+// Whether two tensors of the same shape share memory: with the same strides and type exactly,
+// otherwise by their ranges.
+bool overlap(const csa_vectors &a, const csa_vectors &b, const VectorShape &n) {
+    auto span = [&](const csa_vectors &v) {
+        return ((n.rows - 1) * row_step(v, n) + (n.heads - 1) * head_step(v, n) + n.dim) * dtype_size(v.dtype);
+    };
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.data), pb = reinterpret_cast<uintptr_t>(b.data);
+    if (pa + (uintptr_t)span(a) <= pb || pb + (uintptr_t)span(b) <= pa) return false;
+    const int64_t bytes = (int64_t)pb - (int64_t)pa;
+    if (!same_layout(a, b, n) || bytes % dtype_size(a.dtype) != 0) return true;
+    return meets(bytes / dtype_size(a.dtype), row_step(a, n), head_step(a, n), n, false);
 }
 
 csa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
@@ -295,6 +359,63 @@ csa_status csa_read_device_status(const csa_cache *cache, csa_stream_t stream, i
     if (cudaMemcpy(&v, cache->status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return CSA_ERR_CUDA;
     if (cudaMemcpy(cache->status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return CSA_ERR_CUDA;
     *out_flags = v;
+    return CSA_OK;
+}
+
+csa_status csa_rotary(const csa_vectors *x, const csa_vectors *out, int32_t rows, int32_t heads, int32_t dim,
+                      const csa_rope *rope, const int32_t *pos, int32_t inverse, csa_stream_t stream) {
+    if (!x || !out || !rope) return CSA_ERR_NULL;
+    if (rows < 0 || heads < 1 || dim < 2) return CSA_ERR_SHAPE;
+    if (rope->rot_begin < 0 || rope->rot_dim < 2 || rope->rot_dim % 2 != 0 || rope->rot_begin > dim - rope->rot_dim)
+        return CSA_ERR_SHAPE;
+    if (rope->layout != CSA_ROPE_PAIRS && rope->layout != CSA_ROPE_HALF) return CSA_ERR_SHAPE;
+    if (!dtype_ok(x->dtype) || !dtype_ok(out->dtype)) return CSA_ERR_SHAPE;
+    if (dim > kMaxRotaryDim) return CSA_ERR_UNSUPPORTED;
+    if (rows == 0) return CSA_OK;
+    if (!x->data || !out->data || !rope->inv_freq || !pos) return CSA_ERR_NULL;
+    if (!aligned(x->data, dtype_size(x->dtype)) || !aligned(out->data, dtype_size(out->dtype)) ||
+        !aligned(rope->inv_freq, 4) || !aligned(pos, 4))
+        return CSA_ERR_ALIGN;
+    const VectorShape shape = {rows, heads, dim};
+    if (!strides_ok(*x, shape) || !strides_ok(*out, shape) || self_overlap(*out, shape)) return CSA_ERR_SHAPE;
+    const bool in_place = x->data == out->data && same_layout(*x, *out, shape);
+    if (!in_place && overlap(*x, *out, shape)) return CSA_ERR_SHAPE;
+    return from_cuda(csa::launch_rotary(*x, *out, rows, heads, dim, *rope, pos, inverse != 0, in_place,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, int32_t original_len,
+                                  double beta_fast, double beta_slow, float *inv_freq, float *mscale) {
+    if (!inv_freq) return CSA_ERR_NULL;
+    if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > kMaxRotaryDim || !(base > 1.0) || std::isinf(base))
+        return CSA_ERR_SHAPE;
+    if (scaling < CSA_ROPE_SCALE_NONE || scaling > CSA_ROPE_SCALE_PARTS) return CSA_ERR_SHAPE;
+    if (scaling != CSA_ROPE_SCALE_NONE && (!(factor >= 1.0) || std::isinf(factor))) return CSA_ERR_SHAPE;
+    if (scaling == CSA_ROPE_SCALE_BASE) {
+        if (rot_dim <= 2) return CSA_ERR_SHAPE;
+        base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    }
+    double low = 0, high = 0;
+    if (scaling == CSA_ROPE_SCALE_PARTS) {
+        if (original_len < 1 || !(beta_slow > 0) || !(beta_fast >= beta_slow) || std::isinf(beta_fast))
+            return CSA_ERR_SHAPE;
+        // the pair that turns `beta` times in original_len tokens: original_len * f_p = 2 pi beta
+        auto pair_of = [&](double beta) {
+            return rot_dim * std::log(original_len / (2 * 3.14159265358979323846 * beta)) / (2 * std::log(base));
+        };
+        low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+        high = std::fmin(std::ceil(pair_of(beta_slow)), rot_dim - 1.0);
+    }
+    for (int p = 0; p < rot_dim / 2; ++p) {
+        double f = std::pow(base, -2.0 * p / rot_dim);
+        if (scaling == CSA_ROPE_SCALE_LINEAR) f /= factor;
+        if (scaling == CSA_ROPE_SCALE_PARTS) {
+            const double ramp = std::fmin(std::fmax((p - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+            f = f / factor * ramp + f * (1 - ramp);
+        }
+        inv_freq[p] = (float)f;
+    }
+    if (mscale) *mscale = scaling == CSA_ROPE_SCALE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
     return CSA_OK;
 }
 

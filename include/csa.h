@@ -353,6 +353,76 @@ csa_status hca_decode_attend(const csa_cache *cache, const void *q, int32_t n_qu
                              void *workspace, size_t workspace_bytes, csa_stream_t stream);
 
 /*
+ * Rotary positions. Vector (row i, head h) is `dim` channels at
+ * data + i * row_stride + h * head_stride (strides in elements); the channels
+ * [rot_begin, rot_begin + rot_dim) are turned pairwise by angles that grow with
+ * the row's token position, the others are copied:
+ *   t = pos[i] * inv_freq[p],  0 <= p < rot_dim / 2
+ *   y_a = mscale * (a cos t - b sin t),  y_b = mscale * (a sin t + b cos t)
+ * with (a, b) the channels rot_begin + (2p, 2p + 1) (CSA_ROPE_PAIRS) or
+ * rot_begin + (p, p + rot_dim / 2) (CSA_ROPE_HALF). inverse != 0 turns by -t, with
+ * the same mscale: it takes a rotation back where mscale is 1 (attention
+ * outputs, whose entries are key and value at once), and it is the gradient:
+ * dx = csa_rotary(dy, inverse) for y = csa_rotary(x).
+ * pos * inv_freq is formed and reduced in float64, so any int32 position works;
+ * the arithmetic is float32, rounded once to the output's type.
+ */
+typedef enum { CSA_BF16 = 0, CSA_F32 = 1 } csa_dtype;
+typedef enum { CSA_ROPE_PAIRS = 0, CSA_ROPE_HALF = 1 } csa_rope_layout;
+
+typedef struct {
+    void *data;
+    int32_t dtype; /* csa_dtype */
+    int64_t row_stride, head_stride;
+} csa_vectors;
+
+typedef struct {
+    const float *inv_freq; /* device float32 [rot_dim / 2] */
+    int32_t rot_begin, rot_dim;
+    int32_t layout; /* csa_rope_layout */
+    float mscale;
+} csa_rope;
+
+/*
+ * Arguments: rows >= 0 (0: nothing is launched), heads >= 1, dim 2..8192;
+ * rot_dim even, 2..dim - rot_begin; pos int32 [rows] device.
+ * x is only read; its strides may be 0 (broadcast) or in any order.
+ * out: vectors that do not overlap one another; either x's own storage (in place:
+ * same data, strides and type; only the rotated channels are then touched) or
+ * apart from x, also as disjoint channels of the same rows (same strides and
+ * type). Other overlaps: CSA_ERR_SHAPE. data need only be aligned to its
+ * element; vectors on 16-byte boundaries with a rotated range in whole chunks
+ * of 8 channels are moved 16 bytes at a time, others one channel at a time.
+ */
+csa_status csa_rotary(const csa_vectors *x, const csa_vectors *out, int32_t rows, int32_t heads, int32_t dim,
+                      const csa_rope *rope, const int32_t *pos, int32_t inverse, csa_stream_t stream);
+
+/*
+ * The frequencies of csa_rotary, computed on the host into HOST memory:
+ * f_p = base^(-2p / rot_dim), scaled for contexts `factor` times longer than
+ * original_len tokens:
+ *   CSA_ROPE_SCALE_NONE    f_p as it is (factor, original_len and betas unused)
+ *   CSA_ROPE_SCALE_LINEAR  f_p / factor (position interpolation)
+ *   CSA_ROPE_SCALE_BASE    base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *                          (rot_dim > 2)
+ *   CSA_ROPE_SCALE_PARTS   by parts (YaRN): pairs that turn more than beta_fast
+ *                          times in original_len tokens keep f_p, pairs that
+ *                          turn less than beta_slow times get f_p / factor, with
+ *                          a linear ramp over p between; *mscale = 0.1 ln factor + 1
+ * inv_freq float32 [rot_dim / 2]; *mscale (may be NULL) is 1 but for PARTS.
+ * base > 1, factor >= 1, original_len >= 1, beta_fast >= beta_slow > 0, else CSA_ERR_SHAPE.
+ */
+typedef enum {
+    CSA_ROPE_SCALE_NONE = 0,
+    CSA_ROPE_SCALE_LINEAR = 1,
+    CSA_ROPE_SCALE_BASE = 2,
+    CSA_ROPE_SCALE_PARTS = 3
+} csa_rope_scaling;
+
+csa_status csa_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, int32_t original_len,
+                                  double beta_fast, double beta_slow, float *inv_freq, float *mscale);
+
+/*
  * Waits for `stream`, then copies *cache->status to *out_flags and clears the
  * device word. The only call that synchronizes. Returns CSA_ERR_NULL when
  * cache->status is NULL.
