@@ -9,7 +9,7 @@ is no CPU fallback.
 The function names mirror the C ABI in include/csa.h:
     csa_compress_quantize, csa_index_topk, csa_decode_attend, hca_decode_attend,
     csa_read_device_status (+ the workspace-size queries),
-    csa_rotary, csa_rotary_frequencies.
+    csa_cache_copy, csa_rotary, csa_rotary_frequencies.
 """
 from __future__ import annotations
 
@@ -49,6 +49,7 @@ EXPORTED = (
     "csa_index_topk_noalloc", "csa_index_pool_workspace", "csa_index_topk_pool", "csa_index_reindex_workspace",
     "csa_index_topk_reindex", "csa_index_reindex_layers_workspace", "csa_index_topk_reindex_layers",
     "csa_probe_mxf4_mma", "csa_rotary", "csa_rotary_frequencies",
+    "csa_cache_copy_workspace", "csa_cache_copy",
 )
 
 
@@ -128,6 +129,10 @@ def declare(lib):
     lib.csa_read_device_status.restype = I
     lib.csa_probe_mxf4_mma.argtypes = [I, P, P, ctypes.POINTER(ctypes.c_int64)]
     lib.csa_probe_mxf4_mma.restype = I
+    lib.csa_cache_copy_workspace.argtypes = [CP, I, I]
+    lib.csa_cache_copy_workspace.restype = S
+    lib.csa_cache_copy.argtypes = [CP, CP, I, P, P, P, I, P, P, S, P]
+    lib.csa_cache_copy.restype = I
     VP, D = ctypes.POINTER(_CVectors), ctypes.c_double
     lib.csa_rotary.argtypes = [VP, VP, I, I, I, ctypes.POINTER(_CRope), P, I, P]
     lib.csa_rotary.restype = I
@@ -155,35 +160,31 @@ def _stream(stream):
 
 
 class _On:
-    """The device of a call's tensors made current, and the stream the call goes to: `stream`, or
-    that device's current one. Scratch made inside is kept alive for a stream that is not current."""
+    """The device of a call's tensors made current, and the stream the call goes to made current on
+    it: `stream`, or that device's current one (what the call allocates then belongs to that stream)."""
 
     def __init__(self, device, stream):
         import torch
 
-        self.guard = None
+        self.guard, self.stream = None, stream
         if device.type != "cuda":
             raise CsaError(f"tensors must be on a CUDA device, not {device}")
-        if device.index is not None and device.index != torch.cuda.current_device():
+        if stream is not None:
+            self.guard = torch.cuda.stream(stream)
+        elif device.index is not None and device.index != torch.cuda.current_device():
             self.guard = torch.cuda.device(device)
-        self.device, self.given = device, stream
 
     def __enter__(self):
         import torch
 
         if self.guard is not None:
             self.guard.__enter__()
-        self.stream = torch.cuda.current_stream() if self.given is None else self.given
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        stream = torch.cuda.current_stream() if self.stream is None else self.stream
+        return ctypes.c_void_p(stream.cuda_stream)
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
-
-    def scratch(self, t):
-        if self.given is not None:
-            t.record_stream(self.given)
-        return t
 
 
 def _expect(what, name, t, device, dtype, shape):
@@ -435,6 +436,42 @@ def hca_decode_attend(cache: Cache, q, q_offsets, q_pos, win_kv=None, win_start=
     return out
 
 
+def csa_cache_copy_workspace(dst: Cache, n_jobs: int, keep_cols: int = 0) -> int:
+    return int(load_library().csa_cache_copy_workspace(ctypes.byref(dst.c_struct()), n_jobs, keep_cols))
+
+
+def csa_cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, keep=None, max_blocks=None, workspace=None,
+                   stream=None):
+    """Fork, move, cut, compact or free cache slots: slot dst_slot[i] of dst becomes the blocks of slot
+    src_slot[i] of src (-1: none) -- all of them, the first max_blocks[i], or those listed in keep [n, cols]
+    (ascending, -1 behind the last, as the indexer returns them). Slots and limits are int32 tensors;
+    src may be dst, and a slot its own source (in place)."""
+    import torch
+
+    lib, what = load_library(), "csa_cache_copy"
+    device, n = src.fp4.device, src_slot.shape[0]
+    if dst.fp4.device != device:
+        raise CsaError(f"{what}: src is on {device}, dst on {dst.fp4.device}")
+    _expect(what, "src_slot", src_slot, device, torch.int32, (None,))
+    _expect(what, "dst_slot", dst_slot, device, torch.int32, (n,))
+    cols = 0
+    if keep is not None:
+        _expect(what, "keep", keep, device, torch.int32, (n, None))
+        cols = keep.shape[1]
+        if cols == 0:
+            raise CsaError(f"{what}: keep needs a column (-1 in it keeps nothing)")
+    if max_blocks is not None:
+        _expect(what, "max_blocks", max_blocks, device, torch.int32, (n,))
+    cs = src.c_struct()
+    cd = cs if dst is src else dst.c_struct()
+    with _On(device, stream) as s:
+        if workspace is None:
+            need = lib.csa_cache_copy_workspace(ctypes.byref(cd), n, cols)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        _check(lib.csa_cache_copy(ctypes.byref(cs), ctypes.byref(cd), n, src_slot.data_ptr(), dst_slot.data_ptr(),
+                                  _ptr(keep), cols, _ptr(max_blocks), workspace.data_ptr(), workspace.nbytes, s), what)
+
+
 def _vectors(what, name, t):
     import torch
 
@@ -458,16 +495,17 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
     cx = _vectors(what, "x", x)
     rows, dim = x.shape[0], x.shape[-1]
     heads = x.shape[1] if x.dim() == 3 else 1
-    if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != x.shape or out.device != x.device or (out_dtype is not None and out.dtype != out_dtype):
+    if out is not None and (out.shape != x.shape or out.device != x.device or
+                            (out_dtype is not None and out.dtype != out_dtype)):
         raise CsaError(f"{what}: out must match x's shape and device, and out_dtype")
-    co = _vectors(what, "out", out)
     _expect(what, "pos", pos, x.device, torch.int32, (rows,))
     _expect(what, "inv_freq", inv_freq, x.device, torch.float32, (None,))
     rot = 2 * inv_freq.shape[0]
     rope = _CRope(inv_freq.data_ptr(), dim - rot if rot_begin is None else rot_begin, rot, layout, mscale)
     with _On(x.device, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        co = _vectors(what, "out", out)
         _check(lib.csa_rotary(ctypes.byref(cx), ctypes.byref(co), rows, heads, dim, ctypes.byref(rope),
                               pos.data_ptr(), int(inverse), s), what)
     return out

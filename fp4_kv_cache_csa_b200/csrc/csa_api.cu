@@ -31,6 +31,10 @@ cudaError_t launch_attend(const csa_cache &c, const void *q, int Nq, int H, cons
                           const int32_t *q_pos, const int32_t *sel_idx, int topk, const void *win_kv,
                           const int64_t *win_start, const int32_t *win_len, int max_win, float softmax_scale,
                           float *out, float *lse, void *workspace, int num_ctas, cudaStream_t s);
+size_t cache_copy_workspace_bytes(int dst_batch, int jobs, int cols);
+cudaError_t launch_cache_copy(const csa_cache &src, const csa_cache &dst, int jobs, const int32_t *src_slot,
+                              const int32_t *dst_slot, const int32_t *keep, int cols, const int32_t *max_blocks,
+                              void *workspace, int num_sms, cudaStream_t s);
 cudaError_t launch_rotary(const csa_vectors &x, const csa_vectors &out, int rows, int heads, int dim,
                           const csa_rope &rope, const int32_t *pos, bool inverse, bool in_place, cudaStream_t s);
 }  // namespace csa
@@ -70,6 +74,31 @@ csa_status check_cache(const csa_cache *c) {
         }
     }
     return CSA_OK;
+}
+
+// ---- slot copies (csa_cache_copy)
+constexpr int kMaxCopyDim = 512;
+constexpr int kMaxCopyJobs = 65535;  // a grid dimension
+
+int64_t scale_row(const csa_cache &c) { return c.dim / (c.scale_fmt == CSA_SCALE_E4M3_16 ? 16 : 32); }
+int64_t key_row(const csa_cache &c) {
+    return c.idx_dtype == CSA_IDX_BF16 ? 2 * c.idx_dim : c.idx_dtype == CSA_IDX_E4M3 ? c.idx_dim : c.idx_dim / 2;
+}
+bool ranges_meet(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+// One cache with itself, or two that share nothing.
+bool same_or_apart(const csa_cache &a, const csa_cache &b) {
+    if (a.fp4 == b.fp4 && a.scale == b.scale && a.idx_key == b.idx_key && a.idx_key_scale == b.idx_key_scale &&
+        a.n_blocks == b.n_blocks && a.batch == b.batch && a.capacity == b.capacity)
+        return true;
+    const int64_t na = (int64_t)a.batch * a.capacity, nb = (int64_t)b.batch * b.capacity;
+    return !ranges_meet(a.fp4, na * (a.dim / 2), b.fp4, nb * (b.dim / 2)) &&
+           !ranges_meet(a.scale, na * scale_row(a), b.scale, nb * scale_row(b)) &&
+           !ranges_meet(a.idx_key, na * key_row(a), b.idx_key, nb * key_row(b)) &&
+           !ranges_meet(a.idx_key_scale, na * (a.idx_dim / 32), b.idx_key_scale, nb * (b.idx_dim / 32)) &&
+           !ranges_meet(a.n_blocks, 4 * (int64_t)a.batch, b.n_blocks, 4 * (int64_t)b.batch);
 }
 
 // ---- strided vectors (csa_rotary)
@@ -360,6 +389,37 @@ csa_status csa_read_device_status(const csa_cache *cache, csa_stream_t stream, i
     if (cudaMemcpy(cache->status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return CSA_ERR_CUDA;
     *out_flags = v;
     return CSA_OK;
+}
+
+size_t csa_cache_copy_workspace(const csa_cache *dst, int32_t n_jobs, int32_t keep_cols) {
+    if (!dst || dst->batch < 1 || n_jobs < 0 || n_jobs > kMaxCopyJobs || keep_cols < 0 || keep_cols > kMaxCapacity)
+        return 0;
+    return csa::cache_copy_workspace_bytes(dst->batch, n_jobs, keep_cols);
+}
+
+csa_status csa_cache_copy(const csa_cache *src, const csa_cache *dst, int32_t n_jobs, const int32_t *src_slot,
+                          const int32_t *dst_slot, const int32_t *keep, int32_t keep_cols, const int32_t *max_blocks,
+                          void *workspace, size_t workspace_bytes, csa_stream_t stream) {
+    csa_status st = check_cache(src);
+    if (st != CSA_OK) return st;
+    if ((st = check_cache(dst)) != CSA_OK) return st;
+    if (n_jobs < 0 || keep_cols < 0 || (keep == nullptr) != (keep_cols == 0)) return CSA_ERR_SHAPE;
+    if (src->dim != dst->dim || src->block != dst->block || src->scale_fmt != dst->scale_fmt ||
+        (src->idx_key == nullptr) != (dst->idx_key == nullptr))
+        return CSA_ERR_SHAPE;
+    if (src->idx_key && (src->idx_dim != dst->idx_dim || src->idx_dtype != dst->idx_dtype)) return CSA_ERR_SHAPE;
+    if (n_jobs > kMaxCopyJobs || keep_cols > kMaxCapacity || src->dim > kMaxCopyDim) return CSA_ERR_UNSUPPORTED;
+    if (!same_or_apart(*src, *dst)) return CSA_ERR_SHAPE;
+    if (n_jobs == 0) return CSA_OK;
+    if (!src_slot || !dst_slot) return CSA_ERR_NULL;
+    if (!aligned(src_slot, 4) || !aligned(dst_slot, 4) || !aligned(keep, 4) || !aligned(max_blocks, 4))
+        return CSA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < csa_cache_copy_workspace(dst, n_jobs, keep_cols)) return CSA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CSA_ERR_ALIGN;
+    const int sms = num_sms();
+    if (sms <= 0) return CSA_ERR_CUDA;
+    return from_cuda(csa::launch_cache_copy(*src, *dst, n_jobs, src_slot, dst_slot, keep, keep_cols, max_blocks,
+                                            workspace, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 csa_status csa_rotary(const csa_vectors *x, const csa_vectors *out, int32_t rows, int32_t heads, int32_t dim,

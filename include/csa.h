@@ -353,6 +353,40 @@ csa_status hca_decode_attend(const csa_cache *cache, const void *q, int32_t n_qu
                              void *workspace, size_t workspace_bytes, csa_stream_t stream);
 
 /*
+ * Copies blocks between cache slots: forking a request to several continuations,
+ * moving it to another slot or cache, cutting it short, evicting blocks
+ * (compaction) and freeing it. Job i makes slot dst_slot[i] of dst hold
+ *   keep == NULL: the first n blocks of slot src_slot[i] of src, with n its
+ *                 n_blocks (and at most max_blocks[i]);
+ *   keep != NULL: the blocks of that slot listed in keep[i][0 ..], in order: ascending
+ *                 block indices, -1 behind the last one (the form of sel_idx), at
+ *                 most max_blocks[i] of them. An index at or beyond the source's
+ *                 n_blocks, or not above the one before it, ends the list there
+ *                 and sets CSA_DEV_BAD_INDEX;
+ *   src_slot[i] < 0: nothing (the slot is freed).
+ * Every plane of the block moves bit for bit, and n_blocks[dst_slot[i]] becomes the
+ * number of blocks kept; the destination's bytes behind them stay as they were.
+ *   src, dst   the same cache (all pointers and sizes equal) or caches that share
+ *              no memory, with the same dim, block and formats; batch and capacity
+ *              may differ. dim at most 512.
+ *   src_slot, dst_slot int32 [n_jobs] device; max_blocks int32 [n_jobs] device or NULL
+ *   keep       int32 [n_jobs][keep_cols] device or NULL (then keep_cols is 0)
+ *   n_jobs     0 (nothing is launched) .. 65535
+ *   workspace  >= csa_cache_copy_workspace(dst, n_jobs, keep_cols) bytes, 256-byte aligned
+ * Within one cache src_slot[i] == dst_slot[i] works in place: without a list it only
+ * cuts n_blocks, with one it compacts the slot. Jobs of one call are independent
+ * of each other: all of them see the cache as it was before the call. A job that
+ * would break that -- a slot written by a job before it, or, within one cache, a
+ * slot that another job reads (unless the job only cuts it) -- is skipped and sets
+ * CSA_DEV_BAD_INDEX in dst->status, as does a job with a slot out of range; one
+ * that does not fit dst's capacity is skipped with CSA_DEV_CAPACITY.
+ */
+size_t csa_cache_copy_workspace(const csa_cache *dst, int32_t n_jobs, int32_t keep_cols);
+csa_status csa_cache_copy(const csa_cache *src, const csa_cache *dst, int32_t n_jobs, const int32_t *src_slot,
+                          const int32_t *dst_slot, const int32_t *keep, int32_t keep_cols, const int32_t *max_blocks,
+                          void *workspace, size_t workspace_bytes, csa_stream_t stream);
+
+/*
  * Rotary positions. Vector (row i, head h) is `dim` channels at
  * data + i * row_stride + h * head_stride (strides in elements); the channels
  * [rot_begin, rot_begin + rot_dim) are turned pairwise by angles that grow with
