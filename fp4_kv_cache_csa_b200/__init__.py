@@ -9,7 +9,7 @@ is no CPU fallback.
 The function names mirror the C ABI in include/csa.h:
     csa_compress_quantize, csa_index_topk, csa_decode_attend, hca_decode_attend,
     csa_read_device_status (+ the workspace-size queries),
-    csa_cache_copy, csa_rotary, csa_rotary_frequencies.
+    hca_shared_attend, csa_cache_copy, csa_rotary, csa_rotary_frequencies.
 """
 from __future__ import annotations
 
@@ -49,7 +49,7 @@ EXPORTED = (
     "csa_index_topk_noalloc", "csa_index_pool_workspace", "csa_index_topk_pool", "csa_index_reindex_workspace",
     "csa_index_topk_reindex", "csa_index_reindex_layers_workspace", "csa_index_topk_reindex_layers",
     "csa_probe_mxf4_mma", "csa_rotary", "csa_rotary_frequencies",
-    "csa_cache_copy_workspace", "csa_cache_copy",
+    "csa_cache_copy_workspace", "csa_cache_copy", "hca_shared_attend_workspace", "hca_shared_attend",
 )
 
 
@@ -129,6 +129,10 @@ def declare(lib):
     lib.csa_read_device_status.restype = I
     lib.csa_probe_mxf4_mma.argtypes = [I, P, P, ctypes.POINTER(ctypes.c_int64)]
     lib.csa_probe_mxf4_mma.restype = I
+    lib.hca_shared_attend_workspace.argtypes = [CP, I, I]
+    lib.hca_shared_attend_workspace.restype = S
+    lib.hca_shared_attend.argtypes = [CP, P, I, I, P, P, P, P, ctypes.c_float, P, P, P, S, P]
+    lib.hca_shared_attend.restype = I
     lib.csa_cache_copy_workspace.argtypes = [CP, I, I]
     lib.csa_cache_copy_workspace.restype = S
     lib.csa_cache_copy.argtypes = [CP, CP, I, P, P, P, I, P, P, S, P]
@@ -433,6 +437,49 @@ def hca_decode_attend(cache: Cache, q, q_offsets, q_pos, win_kv=None, win_start=
                                  _ptr(win_kv), _ptr(win_start), _ptr(win_len), max_win, float(softmax_scale),
                                  _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)),
            "hca_decode_attend")
+    return out
+
+
+def hca_shared_attend_workspace(cache: Cache, n_queries: int, heads: int) -> int:
+    return int(load_library().hca_shared_attend_workspace(ctypes.byref(cache.c_struct()), n_queries, heads))
+
+
+def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, join_lse=None,
+                      softmax_scale: Optional[float] = None, out=None, lse=None, workspace=None, stream=None):
+    """Dense attention of many queries over one slot's blocks (a prompt that continuations share, a prefill
+    chunk), each tile dequantized once for 64 (query, head) columns; joined with (join_out, join_lse), the
+    float32 result of a query's own part, as one softmax. Without q_pos every query sees all blocks of its
+    slot. q [Nq, H, D] bf16; returns out [Nq, H, D] bf16, and fills lse [Nq, H] float32 if given."""
+    import torch
+
+    lib, what = load_library(), "hca_shared_attend"
+    device, bf16, f32, i32 = q.device, torch.bfloat16, torch.float32, torch.int32
+    _expect(what, "q", q, device, bf16, (None, None, cache.dim))
+    n, heads, D = q.shape
+    if cache.fp4.device != device:
+        raise CsaError(f"{what}: cache is on {cache.fp4.device}, q on {device}")
+    _expect(what, "q_offsets", q_offsets, device, i32, (cache.batch + 1,))
+    if q_pos is not None:
+        _expect(what, "q_pos", q_pos, device, i32, (n,))
+    if join_out is not None:
+        _expect(what, "join_out", join_out, device, f32, (n, heads, D))
+    if join_lse is not None:
+        _expect(what, "join_lse", join_lse, device, f32, (n, heads))
+    if out is not None:
+        _expect(what, "out", out, device, bf16, (n, heads, D))
+    if lse is not None:
+        _expect(what, "lse", lse, device, f32, (n, heads))
+    c = cache.c_struct()
+    with _On(device, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            need = lib.hca_shared_attend_workspace(ctypes.byref(c), n, heads)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        _check(lib.hca_shared_attend(ctypes.byref(c), q.data_ptr(), n, heads, q_offsets.data_ptr(), _ptr(q_pos),
+                                     _ptr(join_out), _ptr(join_lse), D ** -0.5 if softmax_scale is None else
+                                     softmax_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                                     workspace.nbytes, s), what)
     return out
 
 

@@ -31,6 +31,11 @@ cudaError_t launch_attend(const csa_cache &c, const void *q, int Nq, int H, cons
                           const int32_t *q_pos, const int32_t *sel_idx, int topk, const void *win_kv,
                           const int64_t *win_start, const int32_t *win_len, int max_win, float softmax_scale,
                           float *out, float *lse, void *workspace, int num_ctas, cudaStream_t s);
+size_t shared_attend_workspace_bytes(int batch, int Nq, int H, int D, int num_sms);
+cudaError_t launch_shared_attend(const csa_cache &c, const void *q, int Nq, int H, const int32_t *q_offsets,
+                                 const int32_t *q_pos, const float *join_out, const float *join_lse,
+                                 float softmax_scale, void *out, float *lse, void *workspace, int num_sms,
+                                 cudaStream_t s);
 size_t cache_copy_workspace_bytes(int dst_batch, int jobs, int cols);
 cudaError_t launch_cache_copy(const csa_cache &src, const csa_cache &dst, int jobs, const int32_t *src_slot,
                               const int32_t *dst_slot, const int32_t *keep, int cols, const int32_t *max_blocks,
@@ -389,6 +394,41 @@ csa_status csa_read_device_status(const csa_cache *cache, csa_stream_t stream, i
     if (cudaMemcpy(cache->status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return CSA_ERR_CUDA;
     *out_flags = v;
     return CSA_OK;
+}
+
+size_t hca_shared_attend_workspace(const csa_cache *cache, int32_t n_queries, int32_t heads) {
+    if (!cache || cache->batch < 1 || n_queries < 1 || heads < 1 || heads > 64 ||
+        (cache->dim != 128 && cache->dim != 512))
+        return 0;
+    const int sms = num_sms();
+    if (sms <= 0) return 0;
+    return csa::shared_attend_workspace_bytes(cache->batch, n_queries, heads, cache->dim, sms);
+}
+
+csa_status hca_shared_attend(const csa_cache *cache, const void *q, int32_t n_queries, int32_t heads,
+                             const int32_t *q_offsets, const int32_t *q_pos, const float *join_out,
+                             const float *join_lse, float softmax_scale, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, csa_stream_t stream) {
+    csa_status st = check_cache(cache);
+    if (st != CSA_OK) return st;
+    if (!q || !q_offsets || !out || (join_out == nullptr) != (join_lse == nullptr)) return CSA_ERR_NULL;
+    if (n_queries < 1 || heads < 1) return CSA_ERR_SHAPE;
+    if (heads > 64 || (cache->dim != 128 && cache->dim != 512)) return CSA_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(join_out, 16) || !aligned(q_offsets, 4) || !aligned(q_pos, 4) ||
+        !aligned(join_lse, 4) || !aligned(lse, 4))
+        return CSA_ERR_ALIGN;
+    const int64_t vec = (int64_t)n_queries * heads, n2 = 2 * vec * cache->dim, n4 = 2 * n2;
+    if (ranges_meet(out, n2, q, n2) || ranges_meet(out, n2, join_out, n4) || ranges_meet(out, n2, join_lse, 4 * vec) ||
+        ranges_meet(out, n2, lse, 4 * vec) || ranges_meet(lse, 4 * vec, q, n2) ||
+        ranges_meet(lse, 4 * vec, join_out, n4) || ranges_meet(lse, 4 * vec, join_lse, 4 * vec))
+        return CSA_ERR_SHAPE;
+    const size_t need = hca_shared_attend_workspace(cache, n_queries, heads);
+    if (need == 0) return CSA_ERR_CUDA;
+    if (!workspace || workspace_bytes < need) return CSA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CSA_ERR_ALIGN;
+    return from_cuda(csa::launch_shared_attend(*cache, q, n_queries, heads, q_offsets, q_pos, join_out, join_lse,
+                                               softmax_scale, out, lse, workspace, num_sms(),
+                                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t csa_cache_copy_workspace(const csa_cache *dst, int32_t n_jobs, int32_t keep_cols) {

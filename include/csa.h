@@ -352,6 +352,44 @@ csa_status hca_decode_attend(const csa_cache *cache, const void *q, int32_t n_qu
                              int32_t max_win, float softmax_scale, float *out, float *lse,
                              void *workspace, size_t workspace_bytes, csa_stream_t stream);
 
+/* Bytes of workspace hca_shared_attend needs (0 on bad sizes). */
+size_t hca_shared_attend_workspace(const csa_cache *cache, int32_t n_queries, int32_t heads);
+
+/*
+ * Dense attention of many queries over the blocks of one slot: a prompt shared by
+ * several continuations (one slot holds it once, for all of them), or a prefill
+ * chunk. As hca_decode_attend over the compressed entries, with every tile of
+ * blocks dequantized once for 64 (query, head) columns, no window, bf16 output,
+ * and an optional second part:
+ *   logit_j = softmax_scale * <q[i][h], e_j>,  lse = ln sum_j exp(logit_j),
+ *   out = sum_j exp(logit_j - lse) e_j   over the visible blocks j of slot b,
+ * and with join_out, join_lse -- the result of attention over other entries, such as
+ * a continuation's own blocks and window from hca_decode_attend or
+ * csa_decode_attend -- both parts as one softmax:
+ *   L = ln(exp(lse) + exp(join_lse)),  out = exp(lse - L) out + exp(join_lse - L) join_out
+ * with L as the lse returned. A part without an entry (lse = -inf) has no weight,
+ * whatever its values; with no entry at all out = 0 and lse = -inf.
+ * Arguments:
+ *   q          bf16 [n_queries][heads][dim]   heads 1..64, dim 128 or 512
+ *   q_offsets  int32 [batch+1] device: queries q_offsets[b] .. q_offsets[b+1]-1 attend
+ *              slot b; rows of out and lse outside [q_offsets[0], q_offsets[batch])
+ *              are not written
+ *   q_pos      int32 [n_queries] device: query i sees the blocks
+ *              j < min(floor((q_pos[i]+1)/m), n_blocks[b]); NULL: all n_blocks[b]
+ *   join_out   float32 [n_queries][heads][dim] and join_lse float32 [n_queries][heads],
+ *              or both NULL
+ *   out        bf16 [n_queries][heads][dim]; lse float32 [n_queries][heads] or NULL.
+ *              They may not overlap q, join_out or join_lse (CSA_ERR_SHAPE).
+ *   workspace  >= hca_shared_attend_workspace(cache, n_queries, heads) bytes, 256-byte
+ *              aligned: group records and two float32 partial outputs per SM
+ * Scale bytes of visible blocks are finite ones (an E4M3 NaN scale would reach every
+ * query of its tile).
+ */
+csa_status hca_shared_attend(const csa_cache *cache, const void *q, int32_t n_queries, int32_t heads,
+                             const int32_t *q_offsets, const int32_t *q_pos, const float *join_out,
+                             const float *join_lse, float softmax_scale, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, csa_stream_t stream);
+
 /*
  * Copies blocks between cache slots: forking a request to several continuations,
  * moving it to another slot or cache, cutting it short, evicting blocks
