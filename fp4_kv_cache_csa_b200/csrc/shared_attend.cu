@@ -25,8 +25,7 @@
 //
 // Warp roles (13 warps, one CTA per SM): four dequantize (they also bring the
 // group's queries in), eight do the softmax and the outputs, one thread issues the
-// MMAs (a fourteenth warp or more would cut the registers of a thread from 128 to 96,
-// and the softmax spills). What bounds it at D = 512: M = 128, N = 64 MMAs read 6 KB of operands from
+// MMAs. What bounds it at D = 512: M = 128, N = 64 MMAs read 6 KB of operands from
 // shared memory per 128 x 64 x 16 products, so shared memory (128 B/cycle) holds them to
 // 0.63 of the tensor rate; the 128 KB tile of 128 blocks leaves no room for a second one,
 // so a tile's parts (128 channels each) are replaced as its O^T products release
@@ -49,12 +48,16 @@ constexpr int kCols = 64;   // columns of a group
 constexpr int kSoftmaxWarps = 8, kDequantWarps = 4;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kDequantWarps + 1);
+// 13 warps launch with 128 registers a thread; the softmax hands some to the dequantizing warps, whose
+// rows of the next tile wait in registers
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 120, kDequantRegs = 144;
+static_assert(kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs <= (kSoftmaxWarps + kDequantWarps) * kLaunchRegs,
+              "the split exceeds what the block is launched with");
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 // Row exponents count from B, the largest of the group's first tile in the CTA (127, that is 1, when
 // its rows are all zero), and a row's is at least B - 40: what that flushes to zero lies below
 // 2^-64 of the first tile's scale, and no sum leaves float32's range over all-zero rows (scale byte 0)
 constexpr int kExponentSpan = 40;
-constexpr float kNoRho = -1e30f;  // reference of a column that has not met an entry
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
@@ -75,11 +78,11 @@ struct Cfg {
     static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
 };
 
-// A group of columns: queries q0 .. q0 + nq - 1 of slot b, its tiles [t0, t1) of the flat list.
-struct Group {
+// A group of columns: queries q0 .. q0 + nq - 1 of slot b, its tiles t0 .. t0 + tiles - 1 of the flat list.
+struct __align__(16) Group {
     int b, q0, nq, n_max;  // n_max / n_min: most and fewest visible blocks of its queries
-    int n_min, pad0, pad1, pad2;
-    long long t0, t1;
+    int n_min, tiles;
+    long long t0;
 };
 
 struct SharedArgs {
@@ -134,7 +137,8 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
     long long tcarry = 0, ucarry = 0;
     for (int base = 0; base < NG; base += blockDim.x) {
         const int g = base + threadIdx.x;
-        long long tiles = 0, units = 0;
+        int tiles = 0;
+        long long units = 0;
         Group r = {};
         if (g < NG) {
             int lo = 0, hi = a.batch - 1;  // the slot with gbase[b] <= g < gbase[b + 1]
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
         const long long tin = block_inclusive_scan<long long>(tiles, tmp);
         if (g < NG) {
             r.t0 = tcarry + tin - tiles;
-            r.t1 = tcarry + tin;
+            r.tiles = tiles;
             a.groups[g] = r;
         }
         if (threadIdx.x == blockDim.x - 1) round_total = tin;
@@ -191,9 +195,9 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
             }
             const Group r = a.groups[lo];
             const long long x = ub - a.gunits[lo] - kStartUnits;
-            const long long k = x > 0 ? min((x + kTileUnits / 2) / kTileUnits, r.t1 - r.t0) : 0;
+            const long long k = x > 0 ? min((x + kTileUnits / 2) / kTileUnits, (long long)r.tiles) : 0;
             t = r.t0 + k;
-            first = t == r.t1 && lo + 1 < NG ? lo + 1 : lo;
+            first = k == r.tiles && lo + 1 < NG ? lo + 1 : lo;
         }
         a.cta_t[c] = t;
         if (c < a.G) a.cta_g[c] = first;
@@ -205,10 +209,10 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
 // a tile as long as queries and outputs follow).
 __device__ __forceinline__ int channel_of(int pos) { return pos; }
 
-// One row's codes (128 channels of each part) and its scales, held by one thread.
+// One row's codes (128 channels, two slices, of each part) and its scales, held by one thread.
 template <int D, int SF>
 struct Row {
-    static constexpr int SW = SF == 0 ? Cfg<D>::PARTS : 2 * Cfg<D>::PARTS;  // 32-bit words of scales
+    static constexpr int SW = SF == kScaleE4M3x16 ? 2 * Cfg<D>::PARTS : Cfg<D>::PARTS;  // 32-bit words of scales
     uint4 code[Cfg<D>::PARTS][4];
     uint32_t sc[SW];
     bool valid;
@@ -251,14 +255,13 @@ __device__ __forceinline__ int row_exponent(const uint32_t (&sc)[N]) {
     return (int)(m & 0xFF);
 }
 
-// One part of the row (128 channels, two slices of the buffer) into E', fp16, in the
-// 128-byte-swizzled layout of the MMA.
+// One part of the row (128 channels, two slices) into E', fp16, in the 128-byte-swizzled layout of the MMA.
 template <int D, int SF>
 __device__ __forceinline__ void dequant(const uint4 (&code)[4], const uint32_t (&sc)[Row<D, SF>::SW], int rmax, int p,
-                                        int j, uint8_t *E) {
+                                        int j, uint8_t *part) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {  // 32 channels: half a slice
-        uint8_t *to = E + (2 * p + (v >> 1)) * Cfg<D>::SLICE + (j >> 3) * 1024 + (j & 7) * 128;
+        uint8_t *to = part + (v >> 1) * Cfg<D>::SLICE + (j >> 3) * 1024 + (j & 7) * 128;
         __half2 s2[2];
         if constexpr (SF == kScaleE8M0x32) {
             const int k = (int)((sc[p] >> (8 * v)) & 0xFF) - rmax;  // <= 0
@@ -291,9 +294,76 @@ __device__ __forceinline__ void dequant(const uint4 (&code)[4], const uint32_t (
 }
 
 // ---------------------------------------------------------------- main kernel
+// Two float32 at a time (one instruction for both), and 2^x to 2^-22 relative with results below 2^-126 as zero.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float pow2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A bounded wait of one thread for a barrier's phase; most find it complete.
+__device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity, const volatile int *abort) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done || mbar_wait_ab<false>(smem_u32(bar), parity, abort);
+}
+
+// One lane of the warp, the same one every time (the compiler then knows that a single thread runs).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// tcgen05.mma with descriptors given as a low word (address, leading offset) and a high one that all
+// of an operand's tiles share.
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                    bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}\n"
+        :
+        : "r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
 // B + 127 from what the dequantizing warps found (E8M0).
-__device__ __forceinline__ int base_of(const int (&b)[4]) {
-    const int m = max(max(b[0], b[1]), max(b[2], b[3]));
+__device__ __forceinline__ int base_of(const int (&b)[kDequantWarps]) {
+    int m = b[0];
+#pragma unroll
+    for (int k = 1; k < kDequantWarps; ++k) m = max(m, b[k]);
     return m > 0 ? m : 127;
 }
 
@@ -317,9 +387,10 @@ __device__ __forceinline__ void finish(float rho, float l, bool join, float othe
 
 // Where a role stands in the CTA's range.
 struct Cursor {
-    int g, seg;           // group, and its number within the CTA
-    long long t, end;     // tile, end of the group's tiles within the range
-    bool first;           // first tile of the group within the CTA
+    int g, seg;       // group, and its number within the CTA
+    int lt;           // tile within the group
+    int left, mine;   // tiles left of the range, and of the group within the range (this one included)
+    bool first;       // first tile of the group within the range
 };
 
 // Shared state behind the operand buffers.
@@ -327,7 +398,7 @@ struct Misc {
     uint64_t e_full[3][4], e_free[3][4], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free[2], r_full, drain;
     uint32_t tmem;
     int abort;
-    alignas(16) float rho[kCols], alpha[kCols], fac[kCols], jfac[kCols];
+    alignas(16) float minus_rho[kCols], alpha[kCols], fac[kCols], jfac[kCols];
     float wred[4][kCols];
     float colmul[2][kCols];  // scale_log2 * 2^(sQ + B) of each column, by segment parity
     int nvis[2][kCols];
@@ -366,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ms->abort = 0;
     }
+    if (tid < kCols) ms->minus_rho[tid] = 0.f;
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms->tmem)),
                      "r"(C::TMEM_COLS)
@@ -379,33 +451,40 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     const volatile int *abort = &ms->abort;
     grid_dep_wait();
     grid_dep_launch();
-    const long long t_begin = a.cta_t[blockIdx.x], t_end = a.cta_t[blockIdx.x + 1];
+    const long long t_begin = a.cta_t[blockIdx.x];
+    const int n_tiles = (int)(a.cta_t[blockIdx.x + 1] - t_begin);
 
     auto start = [&]() {
         Cursor c;
         c.g = a.cta_g[blockIdx.x];
         c.seg = 0;
-        c.t = t_begin;
-        c.end = min(t_end, a.groups[c.g].t1);
+        const Group g = a.groups[c.g];
+        c.lt = (int)(t_begin - g.t0);
+        c.left = n_tiles;
+        c.mine = min(n_tiles, g.tiles - c.lt);
         c.first = true;
         return c;
     };
-    // the next tile; the caller checks c.t < t_end
+    // the next tile (the caller checks c.left > 0)
     auto step = [&](Cursor &c) {
-        ++c.t;
+        ++c.lt;
+        --c.left;
+        --c.mine;
         c.first = false;
-        if (c.t >= c.end && c.t < t_end) {
+        if (c.mine == 0 && c.left > 0) {
             ++c.g;
             ++c.seg;
-            c.end = min(t_end, a.groups[c.g].t1);
+            c.lt = 0;
+            c.mine = min(c.left, a.groups[c.g].tiles);
             c.first = true;
         }
     };
 
-    if (t_begin >= t_end) {
+    if (n_tiles <= 0) {
         // nothing to do: fall through to the common end
     } else if (warp < kSoftmaxWarps) {
         // ================================================================ softmax and output
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int j = tid & (kTile - 1), hf = tid >> 7;
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_addr = tmem + lane_off + 32 * hf;
@@ -413,37 +492,48 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         float lsum[32];
         int n = 0;  // tiles done by this CTA
         Cursor c = start();
-        while (c.t < t_end) {
+        while (c.left > 0) {
             const Group gr = a.groups[c.g];
-            const int seg = c.seg, mp = seg & 1;
-            const long long seg_begin = c.t;
+            const int seg = c.seg, mp = seg & 1, lt0 = c.lt;
             bool gave_up = false;
 #pragma unroll
             for (int k = 0; k < 32; ++k) lsum[k] = 0.f;
             while (true) {
                 const bool first = c.first;
                 const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
-                bool ok = mbar_wait_ab<false>(smem_u32(&ms->e_full[buf][0]), use & 1, abort);
-                ok = ok && mbar_wait_ab<false>(smem_u32(&ms->s_full[sb]), (n >> 1) & 1, abort);
+                bool ok = true;
                 if (n >= C::NP)  // P' is free: the O^T product of tile n - NP is done
-                    ok = ok && mbar_wait_ab<false>(smem_u32(&ms->pv_done[(n - C::NP) & 1]), ((n - C::NP) >> 1) & 1, abort);
+                    ok = wait(&ms->pv_done[(n - C::NP) & 1], ((n - C::NP) >> 1) & 1, abort);
+                ok = ok && wait(&ms->e_full[buf][0], use & 1, abort);
+                const float R = ms->rexp[buf][j];  // the row's exponent from B on
+                const float rmul = pow2(R);
+                const float2 rinv = make_float2(pow2(-R), pow2(-R));
+                ok = ok && wait(&ms->s_full[sb], (n >> 1) & 1, abort);
                 tc_fence_after();
-                const float R = ms->rexp[buf][j];
-                const float rmul = exp2f(R);  // R: the row's exponent from B on
-                const int entry = (int)(c.t - gr.t0) * kTile + j;
+                const int entry = c.lt * kTile + j;
                 const bool masked = entry - j + kTile > gr.n_min;
                 float u[32];
-                auto logits = [&]() {  // u of this thread's 32 columns, from S^T; returns the largest u - rho
+                // u + R - rho of this thread's 32 columns. References are set by the group's first tile, and
+                // raised (with O^T and the sums) when a logit exceeds one by more than 8: then once more from
+                // the start, with the new ones. (A second raise happens only where a logit is so large that
+                // the first one was rounded.) A wait that ran out comes this way too.
+                for (int pass = 0;; ++pass) {
                     float over = -INFINITY;
                     tmem_ld32(s_addr + kCols * sb, u);
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         const float4 cm = *reinterpret_cast<const float4 *>(&ms->colmul[mp][32 * hf + k]);
-                        const float4 rh = *reinterpret_cast<const float4 *>(&ms->rho[32 * hf + k]);
-                        u[k] = fmaf(u[k], cm.x * rmul, R);
-                        u[k + 1] = fmaf(u[k + 1], cm.y * rmul, R);
-                        u[k + 2] = fmaf(u[k + 2], cm.z * rmul, R);
-                        u[k + 3] = fmaf(u[k + 3], cm.w * rmul, R);
+                        const float4 rh = *reinterpret_cast<const float4 *>(&ms->minus_rho[32 * hf + k]);
+                        const float2 rm = make_float2(rmul, rmul), r2 = make_float2(R, R);
+                        // (two roundings, so that the entry that set a reference is at 0 exactly)
+                        const float2 x = add2(fma2(make_float2(u[k], u[k + 1]), mul2(make_float2(cm.x, cm.y), rm), r2),
+                                              make_float2(rh.x, rh.y));
+                        const float2 y = add2(fma2(make_float2(u[k + 2], u[k + 3]), mul2(make_float2(cm.z, cm.w), rm), r2),
+                                              make_float2(rh.z, rh.w));
+                        u[k] = x.x;
+                        u[k + 1] = x.y;
+                        u[k + 2] = y.x;
+                        u[k + 3] = y.y;
                         if (masked) {
                             const int4 nv = *reinterpret_cast<const int4 *>(&ms->nvis[mp][32 * hf + k]);
                             if (entry >= nv.x) u[k] = -INFINITY;
@@ -451,16 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                             if (entry >= nv.z) u[k + 2] = -INFINITY;
                             if (entry >= nv.w) u[k + 3] = -INFINITY;
                         }
-                        over = fmaxf(over, fmaxf(fmaxf(u[k] - rh.x, u[k + 1] - rh.y), fmaxf(u[k + 2] - rh.z, u[k + 3] - rh.w)));
+                        over = fmaxf(over, fmaxf(fmaxf(u[k], u[k + 1]), fmaxf(u[k + 2], u[k + 3])));
                     }
-                    return over;
-                };
-                const float over = logits();
-                // references: set by the group's first tile, raised (with O^T and the sums) when a
-                // logit exceeds one by more than 8; a wait that ran out comes this way too
-                if (bar_or_n<kSoftmaxThreads>(first || over > 8.f || !ok)) {
-                    if (!first && n > 0)
-                        ok = ok && mbar_wait_ab<false>(smem_u32(&ms->pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort);
+                    const bool set = first && pass == 0;
+                    if (!bar_or_n<kSoftmaxThreads>(set || over > 8.f || !ok) || pass == 4) break;
+                    if (!first) ok = ok && wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
                     transpose_reduce32<true>(u);  // lane L: column 32 hf + L over this warp's entries
                     ms->wred[warp & 3][32 * hf + lane] = u[0];
                     if (bar_or_n<kSoftmaxThreads>(!ok)) {
@@ -471,36 +556,32 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     if (tid < kCols) {
                         const float M = fmaxf(fmaxf(ms->wred[0][tid], ms->wred[1][tid]),
                                               fmaxf(ms->wred[2][tid], ms->wred[3][tid]));
-                        float al = 1.f;
-                        if (first) {
-                            ms->rho[tid] = fmaxf(M, kNoRho);
-                        } else if (M > ms->rho[tid] + 8.f) {
-                            al = exp2f(ms->rho[tid] - M);
-                            ms->rho[tid] = M;
-                        }
-                        ms->alpha[tid] = al;
+                        // (a column that sees nothing of its first tile sees nothing of the others)
+                        const bool raise = set ? M > -INFINITY : M > 8.f;
+                        if (raise) ms->minus_rho[tid] -= M;
+                        ms->alpha[tid] = raise ? pow2(-M) : 1.f;
                     }
                     bar_sync_n<kSoftmaxThreads>();
                     if (!first) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int dt = 0; dt < C::PARTS; ++dt) {
-                            float o[32];
-                            tmem_ld32(o_addr + kCols * dt, o);
+                        for (int dt = 0; dt < 2 * C::PARTS; ++dt) {
+                            float o[16];
+                            const uint32_t at = o_addr + kCols * (dt >> 1) + 16 * (dt & 1);
+                            tmem_ld16(at, o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= ms->alpha[32 * hf + k];
-                            tmem_st32(o_addr + kCols * dt, o);
+                            for (int k = 0; k < 16; ++k) o[k] *= ms->alpha[32 * hf + 16 * (dt & 1) + k];
+                            tmem_st16(at, o);
                         }
 #pragma unroll
                         for (int k = 0; k < 32; ++k) lsum[k] *= ms->alpha[32 * hf + k];
                     }
-                    logits();  // again: the reduction used them up (rare, and cheaper than registers for both)
                 }
+                if (gave_up) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[sb]));
-                // P' = 2^(u - rho), fp16, and the row sums (without 2^R_j, which P' carries for E')
-                const float rinv = exp2f(-R);
+                // P' = 2^(u - rho), fp16, and the row sums (without 2^R, which P' carries for E')
                 uint8_t *Pn = P + (n % C::NP) * C::P_BYTES + (j >> 3) * 1024 + (j & 7) * 128;
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
@@ -508,12 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
 #pragma unroll
                     for (int q2 = 0; q2 < 4; ++q2) {
                         const int k = 8 * cc + 2 * q2;
-                        const float2 rh = *reinterpret_cast<const float2 *>(&ms->rho[32 * hf + k]);
-                        const float p0 = exp2f(u[k] - rh.x), p1 = exp2f(u[k + 1] - rh.y);
-                        const __half2 hh = __floats2half2_rn(p0, p1);
+                        const float2 pp = make_float2(pow2(u[k]), pow2(u[k + 1]));
+                        const __half2 hh = __floats2half2_rn(pp.x, pp.y);
                         pk[q2] = *reinterpret_cast<const uint32_t *>(&hh);
-                        lsum[k] = fmaf(p0, rinv, lsum[k]);
-                        lsum[k + 1] = fmaf(p1, rinv, lsum[k + 1]);
+                        const float2 sum = fma2(pp, rinv, make_float2(lsum[k], lsum[k + 1]));
+                        lsum[k] = sum.x;
+                        lsum[k + 1] = sum.y;
                     }
                     *reinterpret_cast<uint4 *>(Pn + (((4 * hf + cc) ^ (j & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
@@ -522,29 +603,30 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[n % C::NP]));
                 ++n;
+                const bool last = c.mine == 1;
                 step(c);
-                if (c.first || c.t >= t_end) break;  // the group's last tile here
+                if (last) break;
             }
             if (gave_up) break;
             // ---------------- the group's output, or its partial
             transpose_reduce32<false>(lsum);
             ms->wred[warp & 3][32 * hf + lane] = lsum[0];
-            const bool ok = mbar_wait_ab<false>(smem_u32(&ms->pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort);
+            const bool ok = wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
             if (bar_or_n<kSoftmaxThreads>(!ok)) {
                 ms->abort = 1;
                 break;
             }
-            const bool whole = seg_begin == gr.t0 && min(t_end, gr.t1) == gr.t1;
+            const bool whole = lt0 == 0 && (c.left > 0 ? c.lt == 0 : c.lt == gr.tiles);
             const int cols = gr.nq * a.H;
             const size_t row0 = (size_t)gr.q0 * a.H;
             // O^T holds E' = e 2^-(R - B) times P' over 2^B
             const float unit = SF == kScaleE8M0x32 ? exp2f((float)(base_of(ms->base[mp]) - 127)) : exp2f(7.f);
-            const int slot = 2 * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
+            const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
             if (tid < kCols) {
                 const float l = ms->wred[0][tid] + ms->wred[1][tid] + ms->wred[2][tid] + ms->wred[3][tid];
-                const float rho = ms->rho[tid];
+                const float rho = -ms->minus_rho[tid];
                 if (!whole) {
-                    a.part_rho[(size_t)slot * kCols + tid] = rho;
+                    a.part_rho[(size_t)slot * kCols + tid] = l == 0.f ? -INFINITY : rho;
                     a.part_l[(size_t)slot * kCols + tid] = l;
                 } else if (tid < cols) {
                     float lse, f, jf;
@@ -594,33 +676,38 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     }
                 }
             }
-            bar_sync_n<kSoftmaxThreads>();  // rho, fac, wred belong to the next group from here on
+            if (tid < kCols) ms->minus_rho[tid] = 0.f;
+            bar_sync_n<kSoftmaxThreads>();  // minus_rho, fac, wred belong to the next group from here on
         }
     } else if (warp < kMmaWarp) {
         // ================================================================ dequantization, queries
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDequantRegs));
         const int j = tid - kSoftmaxThreads, dw = warp - kSoftmaxWarps;
         Row<D, SF> r;
         Cursor c = start();
-        Group gr = a.groups[c.g];
+        int slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;
         // the row this thread dequantizes in a tile of a group, or -1
-        auto row_of = [&](const Group &g, long long t) -> long long {
-            const int e = (int)(t - g.t0) * kTile + j;
-            return e < g.n_max ? (long long)g.b * a.cap + e : -1;
+        auto row_of = [&](int b, int most, int lt) -> long long {
+            const int e = lt * kTile + j;
+            return e < most ? (long long)b * a.cap + e : -1;
         };
-        long long row = row_of(gr, c.t);
-        r.valid = row >= 0;
-        if (r.valid) {
-            load_scales<D, SF>(a, row, r);
+        {
+            const long long row = row_of(slot, n_max, c.lt);
+            r.valid = row >= 0;
+            if (r.valid) {
+                load_scales<D, SF>(a, row, r);
 #pragma unroll
-            for (int p = 0; p < C::PARTS; ++p) load_codes<D, SF>(a, row, p, r);
+                for (int p = 0; p < C::PARTS; ++p) load_codes<D, SF>(a, row, p, r);
+            }
         }
         int n = 0, base = 127 + 7;
         bool ok = true;
-        while (c.t < t_end) {
+        while (c.left > 0) {
             if (c.first) {
+                const Group gr = a.groups[c.g];
                 // the queries of the group: column = row q0 * H + column of q; per column 2^-sQ
-                if (c.seg >= 1) ok = mbar_wait_ab<false>(smem_u32(&ms->q_free), (c.seg - 1) & 1, abort);
-                if (c.seg >= 2) ok = ok && mbar_wait_ab<false>(smem_u32(&ms->o_free[c.seg & 1]), ((c.seg - 2) >> 1) & 1, abort);
+                if (c.seg >= 1) ok = wait(&ms->q_free, (c.seg - 1) & 1, abort);
+                if (c.seg >= 2) ok = ok && wait(&ms->o_free[c.seg & 1], ((c.seg - 2) >> 1) & 1, abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const int cols = gr.nq * a.H, mp = c.seg & 1;
                 if constexpr (SF == kScaleE8M0x32) {  // B, from the rows of the group's first tile
@@ -629,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                         ms->base[mp][dw] = mine;
                         mbar_arrive(smem_u32(&ms->r_full));
                     }
-                    ok = mbar_wait_ab<false>(smem_u32(&ms->r_full), c.seg & 1, abort);
+                    ok = wait(&ms->r_full, c.seg & 1, abort);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     base = base_of(ms->base[mp]);
                 }
@@ -638,10 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 constexpr int CH = D / 8 / LANES;              // 16-byte chunks of a lane
                 const int sub = lane / LANES, sl = lane % LANES;
 #pragma unroll 1
-                for (int k0 = 0; k0 < kCols / kDequantWarps; k0 += 4 * PER) {
-                    uint4 v[4][CH];
+                for (int k0 = 0; k0 < kCols / kDequantWarps; k0 += 2 * PER) {
+                    uint4 v[2][CH];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
                         const int col = dw * (kCols / kDequantWarps) + k0 + x * PER + sub;
                         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((size_t)gr.q0 * a.H + col) * D);
 #pragma unroll
@@ -649,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                             v[x][y] = col < cols ? __ldg(src + sl + y * LANES) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
                         const int col = dw * (kCols / kDequantWarps) + k0 + x * PER + sub;
                         // max |q| as the largest bit pattern (bf16 magnitudes order like integers)
                         uint32_t mx = 0;
@@ -691,27 +778,29 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             // the tile after this one, whose rows are loaded as this one's registers empty
             Cursor nx = c;
             step(nx);
-            const bool more = nx.t < t_end;
-            Group gn = gr;
-            if (more && nx.first) gn = a.groups[nx.g];
-            const long long row_n = more ? row_of(gn, nx.t) : -1;
+            if (nx.left > 0 && nx.first) {
+                slot = a.groups[nx.g].b;
+                n_max = a.groups[nx.g].n_max;
+            }
+            const long long row_n = nx.left > 0 ? row_of(slot, n_max, nx.lt) : -1;
 
             const int buf = n % C::NBUF, use = n / C::NBUF;
             uint8_t *En = E + buf * C::E_BYTES;
             const bool valid = r.valid;
             const int rmax = SF == kScaleE8M0x32 && valid ? max(row_exponent(r.sc), base - kExponentSpan) : base;
+            // (a part at a time, without leaving the loop early, so that the codes stay in registers)
 #pragma unroll
             for (int p = 0; p < C::PARTS; ++p) {
-                if (use >= 1) ok = mbar_wait_ab<false>(smem_u32(&ms->e_free[buf][p]), (use - 1) & 1, abort);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort) && ok;
                 if (p == 0) ms->rexp[buf][j] = (float)(rmax - base);
+                uint8_t *to = En + 2 * p * C::SLICE;
                 if (valid) {
-                    dequant<D, SF>(r.code[p], r.sc, rmax, p, j, En);
+                    dequant<D, SF>(r.code[p], r.sc, rmax, p, j, to);
                 } else {
-                    uint8_t *to = En + 2 * p * C::SLICE + (j >> 3) * 1024 + (j & 7) * 128;
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        *reinterpret_cast<uint4 *>(to + (k >> 3) * C::SLICE + ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(to + (k >> 3) * C::SLICE + (j >> 3) * 1024 + (j & 7) * 128 +
+                                                   ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -723,70 +812,82 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             if (r.valid) load_scales<D, SF>(a, row_n, r);
             ++n;
             c = nx;
-            gr = gn;
         }
         if (!ok) ms->abort = 1;
-    } else if (lane == 0) {  // (the warp's other lanes wait at the common end)
+    } else if (elect_one()) {  // (the warp's other lanes wait at the common end)
         // ================================================================ MMA issue
         constexpr uint32_t IDESC_S = idesc_f16(kTile, kCols, false, false);
         constexpr uint32_t IDESC_O = idesc_f16(kTile, kCols, true, true);
-        const uint32_t E_s = smem_u32(E), Q_s = smem_u32(Q), P_s = smem_u32(P);
+        // operand descriptors: E' and Q' by channels (S^T), E' and P' by blocks (O^T); 16 bytes a unit
+        const uint64_t de = desc_sw128(smem_u32(E), 16, 1024), dq = desc_sw128(smem_u32(Q), 16, 1024);
+        const uint64_t dv = desc_sw128(smem_u32(E), C::SLICE, 1024), dp = desc_sw128(smem_u32(P), 8192, 1024);
+        const uint32_t e_hi = (uint32_t)(de >> 32), q_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32),
+                       p_hi = (uint32_t)(dp >> 32);
         bool ok = true;
         // S^T of tile n
-        auto score = [&](int n, const Cursor &c, bool last) {
+        auto score = [&](int n, bool first, bool last, int seg) {
             const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
-            if (c.first) ok = ok && mbar_wait_ab<false>(smem_u32(&ms->q_full), c.seg & 1, abort);
-            if (n >= 2) ok = ok && mbar_wait_ab<false>(smem_u32(&ms->s_free[sb]), ((n >> 1) - 1) & 1, abort);
+            uint32_t a_lo = (uint32_t)de + buf * (C::E_BYTES >> 4), b_lo = (uint32_t)dq;
+            const uint32_t d = tmem + kCols * sb;
+            if (first) ok = ok && wait(&ms->q_full, seg & 1, abort);
+            if (n >= 2) ok = ok && wait(&ms->s_free[sb], ((n >> 1) - 1) & 1, abort);
+#pragma unroll 1
             for (int p = 0; p < C::PARTS; ++p) {
-                ok = ok && mbar_wait_ab<false>(smem_u32(&ms->e_full[buf][p]), use & 1, abort);
+                ok = ok && wait(&ms->e_full[buf][p], use & 1, abort);
                 if (!ok) return;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {  // 16 channels each
-                    const int sl = 2 * p + (kk >> 2);
-                    const uint64_t da = desc_sw128(E_s + buf * C::E_BYTES + sl * C::SLICE + (kk & 3) * 32, 16, 1024);
-                    const uint64_t db = desc_sw128(Q_s + sl * C::QSLICE + (kk & 3) * 32, 16, 1024);
-                    mma_f16(tmem + kCols * sb, da, db, IDESC_S, p > 0 || kk > 0);
-                }
+                for (int kk = 0; kk < 8; ++kk)  // 16 channels each, 64 of a slice
+                    mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi,
+                        b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4), q_hi, IDESC_S, kk > 0 || p > 0);
+                a_lo += 2 * C::SLICE >> 4;
+                b_lo += 2 * C::QSLICE >> 4;
             }
             mma_commit(smem_u32(&ms->s_full[sb]));
             if (last) mma_commit(smem_u32(&ms->q_free));
         };
         // O^T += of tile n
-        auto value = [&](int n, const Cursor &c) {
+        auto value = [&](int n, bool first, int seg) {
             const int buf = n % C::NBUF;
-            ok = ok && mbar_wait_ab<false>(smem_u32(&ms->p_full[n % C::NP]), (n / C::NP) & 1, abort);
-            if (c.first && c.seg >= 1) ok = ok && mbar_wait_ab<false>(smem_u32(&ms->o_free[(c.seg - 1) & 1]), ((c.seg - 1) >> 1) & 1, abort);
+            uint32_t a_lo = (uint32_t)dv + buf * (C::E_BYTES >> 4), d = tmem + C::TMEM_O;
+            const uint32_t b_lo = (uint32_t)dp + (n % C::NP) * (C::P_BYTES >> 4);
+            ok = ok && wait(&ms->p_full[n % C::NP], (n / C::NP) & 1, abort);
+            if (first && seg >= 1) ok = ok && wait(&ms->o_free[(seg - 1) & 1], ((seg - 1) >> 1) & 1, abort);
             if (!ok) return;
             tc_fence_after();
 #pragma unroll 1
             for (int p = 0; p < C::PARTS; ++p) {
 #pragma unroll
-                for (int kj = 0; kj < kTile / 16; ++kj) {  // 16 blocks each
-                    const uint64_t da = desc_sw128(E_s + buf * C::E_BYTES + 2 * p * C::SLICE + kj * 2048, C::SLICE, 1024);
-                    const uint64_t db = desc_sw128(P_s + (n % C::NP) * C::P_BYTES + kj * 2048, 8192, 1024);
-                    mma_f16(tmem + C::TMEM_O + kCols * p, da, db, IDESC_O, !c.first || kj > 0);
-                }
+                for (int kj = 0; kj < kTile / 16; ++kj)  // 16 blocks each
+                    mma(d, a_lo + (kj * 2048 >> 4), v_hi, b_lo + (kj * 2048 >> 4), p_hi, IDESC_O, kj > 0 || !first);
                 mma_commit(smem_u32(&ms->e_free[buf][p]));
+                a_lo += 2 * C::SLICE >> 4;
+                d += kCols;
             }
             mma_commit(smem_u32(&ms->pv_done[n & 1]));
         };
-        Cursor cs = start(), cv = cs;
-        int ns = 0, nv = 0;
-        while (cv.t < t_end && ok) {
-            // with several tile buffers S^T runs one tile ahead of O^T
-            while (ok && cs.t < t_end && ns < nv + (C::NBUF > 1 ? 2 : 1)) {
-                Cursor nx = cs;
-                step(nx);
-                score(ns, cs, nx.first || nx.t >= t_end);
-                cs = nx;
-                ++ns;
+        int n = 0, left = n_tiles, g = a.cta_g[blockIdx.x], seg = 0;
+        int mine = min(left, (int)(a.groups[g].t0 + a.groups[g].tiles - t_begin));
+        bool before = false;  // the tile before was its group's first (several buffers: its O^T product is due)
+        while (left > 0 && ok) {
+            const int tiles = mine;
+            for (int k = 0; k < tiles && ok; ++k, ++n) {
+                score(n, k == 0, k == tiles - 1, seg);
+                if constexpr (C::NBUF == 1) {
+                    value(n, k == 0, seg);
+                } else {  // S^T runs one tile ahead of O^T
+                    if (n > 0) value(n - 1, before, k == 0 ? seg - 1 : seg);
+                    before = k == 0;
+                }
             }
-            if (!ok) break;
-            value(nv, cv);
-            step(cv);
-            ++nv;
+            left -= tiles;
+            if (left > 0) {
+                ++g;
+                ++seg;
+                mine = min(left, a.groups[g].tiles);
+            }
         }
+        if (C::NBUF > 1 && ok) value(n - 1, before, seg);
         if (!ok) {
             ms->abort = 1;
             // nothing issued may still run when the CTA leaves
@@ -820,10 +921,11 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(SharedArgs a, int D) 
     int lo = 0, hi = NG - 1;  // the group that holds tile tb - 1
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (a.groups[mid].t1 < tb) lo = mid + 1; else hi = mid;
+        if (a.groups[mid].t0 + a.groups[mid].tiles < tb) lo = mid + 1; else hi = mid;
     }
     const Group gr = a.groups[lo];
-    if (tb <= gr.t0 || tb >= gr.t1) return;              // the boundary lies between two groups
+    const long long t1 = gr.t0 + gr.tiles;
+    if (tb <= gr.t0 || tb >= t1) return;              // the boundary lies between two groups
     if (c > 1 && a.cta_t[c - 1] > gr.t0) return;         // an earlier CTA begins inside the group, too
     const int cols = gr.nq * a.H, c0 = blockIdx.y * kMergeCols;
     if (c0 >= cols) return;
@@ -836,13 +938,13 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(SharedArgs a, int D) 
             long long rb = 0;
             if (cc < a.G) {
                 rb = a.cta_t[cc];
-                has = rb < a.cta_t[cc + 1] && rb < gr.t1 && a.cta_t[cc + 1] > gr.t0;
+                has = rb < a.cta_t[cc + 1] && rb < t1 && a.cta_t[cc + 1] > gr.t0;
             }
             const uint32_t mask = __ballot_sync(0xffffffffu, has);
             const int pos = np + __popc(mask & ((1u << threadIdx.x) - 1u));
             if (has && pos < kMostParts) slots[pos] = 2 * cc + (rb >= gr.t0 ? 0 : 1);
             np += __popc(mask);
-            if (!__any_sync(0xffffffffu, cc < a.G && rb < gr.t1)) break;
+            if (!__any_sync(0xffffffffu, cc < a.G && rb < t1)) break;
         }
         if (threadIdx.x == 0) np_s = min(np, kMostParts);
     }
@@ -857,7 +959,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(SharedArgs a, int D) 
         float l = 0.f;
         for (int p = lane; p < np; p += 32) {
             const size_t at = (size_t)slots[p] * kCols + c0 + hh;
-            const float w = exp2f(a.part_rho[at] - top);
+            const float w = top == -INFINITY ? 0.f : exp2f(a.part_rho[at] - top);
             wts[p * kMergeCols + hh] = w;
             l = fmaf(w, a.part_l[at], l);
         }
