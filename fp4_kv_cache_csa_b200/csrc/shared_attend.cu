@@ -23,7 +23,7 @@
 // rounded to fp16's 11 bits, which leaves about 1e-4 of the output's norm, an order
 // below the bf16 rounding of the output. Row sums, references and accumulators are float32.
 //
-// Warp roles (13 warps, one CTA per SM): four dequantize (they also bring the
+// Warp roles (17 warps, one CTA per SM): eight dequantize (they also bring the
 // group's queries in), eight do the softmax and the outputs, one thread issues the
 // MMAs. What bounds it at D = 512: M = 128, N = 64 MMAs read 6 KB of operands from
 // shared memory per 128 x 64 x 16 products, so shared memory (128 B/cycle) holds them to
@@ -45,14 +45,10 @@ namespace {
 
 constexpr int kTile = 128;  // blocks of a tile
 constexpr int kCols = 64;   // columns of a group
-constexpr int kSoftmaxWarps = 8, kDequantWarps = 4;
+constexpr int kSoftmaxWarps = 8, kDequantWarps = 8;  // the latter in two teams of four
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kDequantWarps + 1);
-// 13 warps launch with 128 registers a thread; the softmax hands some to the dequantizing warps, whose
-// rows of the next tile wait in registers
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 120, kDequantRegs = 144;
-static_assert(kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs <= (kSoftmaxWarps + kDequantWarps) * kLaunchRegs,
-              "the split exceeds what the block is launched with");
+constexpr int kTeamWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 // Row exponents count from B, the largest of the group's first tile in the CTA (127, that is 1, when
 // its rows are all zero), and a row's is at least B - 40: what that flushes to zero lies below
@@ -72,8 +68,8 @@ struct Cfg {
     static constexpr int P_BYTES = kTile * kCols * 2;
     static constexpr int SLICE = kTile * 128;            // 64 channels of a tile
     static constexpr int QSLICE = kCols * 128;           // 64 channels of the queries
-    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T
-    static constexpr int TMEM_COLS = TMEM_O + PARTS * kCols <= 256 ? 256 : 512;
+    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T, then the row sums
+    static constexpr int TMEM_COLS = TMEM_O + (PARTS + 1) * kCols <= 256 ? 256 : 512;
     static constexpr int MISC = 6144;
     static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
 };
@@ -205,91 +201,86 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
 }
 
 // ---------------------------------------------------------------- operands
-// The channel that lane position `pos` of a d-tile holds (dequantization may permute channels within
-// a tile as long as queries and outputs follow).
-__device__ __forceinline__ int channel_of(int pos) { return pos; }
-
-// One row's codes (128 channels, two slices, of each part) and its scales, held by one thread.
-template <int D, int SF>
-struct Row {
-    static constexpr int SW = SF == kScaleE4M3x16 ? 2 * Cfg<D>::PARTS : Cfg<D>::PARTS;  // 32-bit words of scales
-    uint4 code[Cfg<D>::PARTS][4];
-    uint32_t sc[SW];
-    bool valid;
+// Four neighbouring lanes share a row: lane v of them takes its 32-channel group v of every part (128 channels,
+// 64 bytes of codes), so that a warp's 16-byte load covers whole 64-byte pieces of eight rows.
+// Scale words: E8M0, one word per part: lane v holds the word of part v (D = 512) or the row's only one;
+// E4M3, two words per part: likewise.
+struct Scales {
+    uint32_t x, y;
 };
 
 template <int D, int SF>
-__device__ __forceinline__ void load_scales(const SharedArgs &a, size_t row, Row<D, SF> &r) {
-    constexpr int SW = Row<D, SF>::SW;
-    const uint8_t *src = a.scale + row * (4 * SW);
-    if constexpr (SW >= 4) {
-#pragma unroll
-        for (int k = 0; k < SW; k += 4) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src) + k / 4);
-            r.sc[k] = u.x;
-            r.sc[k + 1] = u.y;
-            r.sc[k + 2] = u.z;
-            r.sc[k + 3] = u.w;
-        }
+__device__ __forceinline__ Scales load_scales(const SharedArgs &a, size_t row, int v) {
+    constexpr int WORDS = SF == kScaleE4M3x16 ? 2 : 1;  // of a part
+    const uint8_t *src = a.scale + row * (4 * WORDS * Cfg<D>::PARTS) + (D == 512 ? 4 * WORDS * v : 0);
+    Scales r;
+    r.x = __ldg(reinterpret_cast<const uint32_t *>(src));
+    r.y = WORDS == 2 ? __ldg(reinterpret_cast<const uint32_t *>(src) + 1) : 0;
+    return r;
+}
+
+// A load that is issued where it stands (left to itself it is moved down to its use, a part later).
+__device__ __forceinline__ uint4 load_here(const uint8_t *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// The largest byte of a row's scale words.
+__device__ __forceinline__ int row_exponent(uint32_t word) {
+    uint32_t m = __vmaxu4(word, word >> 16);
+    m = max(m & 0xFF, (m >> 8) & 0xFF);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return (int)max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// Eight E2M1 codes to four fp16 pairs. (One conversion takes any byte of a register as it is; the header's
+// function for a byte value first cuts it out: 8 instead of about 14 instructions a word with the scaling.)
+__device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&o)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+
+// This lane's 32 channels of one part of a row, as fp16 into its 128-byte-swizzled place: four 16-byte stores, the
+// second slice's in another order than the first's so that eight lanes meet eight banks. to: the row's
+// place in this lane's slice, off: the four offsets.
+template <int SF>
+__device__ __forceinline__ void dequant(const uint4 &code, Scales sc, int rmax, int v, const uint32_t (&off)[4],
+                                        uint32_t to) {
+    __half2 s2[2];
+    const bool second = (v & 2) != 0;
+    if constexpr (SF == kScaleE8M0x32) {
+        const int k = (int)((sc.x >> (8 * v)) & 0xFF) - rmax;  // <= 0
+        // 2^k in fp16: normal for k >= -14, subnormal down to -24, else 0
+        const uint32_t hb = k >= -14 ? (uint32_t)(k + 15) << 10 : k >= -24 ? 1u << (k + 24) : 0u;
+        const uint32_t h2 = hb * 0x10001u;
+        s2[0] = s2[1] = *reinterpret_cast<const __half2 *>(&h2);
     } else {
+        // E' = e 2^-7
+        const uint32_t bytes = (second ? sc.y : sc.x) >> (16 * (v & 1));
 #pragma unroll
-        for (int k = 0; k < SW; ++k) r.sc[k] = __ldg(reinterpret_cast<const uint32_t *>(src) + k);
+        for (int h = 0; h < 2; ++h) {
+            const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)((bytes >> (8 * (second ? 1 - h : h))) & 0xFF), __NV_E4M3);
+            const __half s = __hmul(__half(hr), __ushort_as_half((uint16_t)((15 - 7) << 10)));
+            s2[h] = __halves2half2(s, s);
+        }
     }
-}
-
-template <int D, int SF>
-__device__ __forceinline__ void load_codes(const SharedArgs &a, size_t row, int p, Row<D, SF> &r) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.fp4 + row * (D / 2) + p * 64);
+    const uint32_t w[4] = {second ? code.z : code.x, second ? code.w : code.y, second ? code.x : code.z,
+                           second ? code.y : code.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r.code[p][k] = __ldg(src + k);
-}
-
-// The largest scale exponent byte of the row (E8M0).
-template <int N>
-__device__ __forceinline__ int row_exponent(const uint32_t (&sc)[N]) {
-    uint32_t m = sc[0];
+    for (int k = 0; k < 4; ++k) {
+        uint32_t o[4];
+        e2m1_halves(w[k], o);
 #pragma unroll
-    for (int k = 1; k < N; ++k) m = __vmaxu4(m, sc[k]);
-    m = __vmaxu4(m, m >> 16);
-    m = __vmaxu4(m, m >> 8);
-    return (int)(m & 0xFF);
-}
-
-// One part of the row (128 channels, two slices) into E', fp16, in the 128-byte-swizzled layout of the MMA.
-template <int D, int SF>
-__device__ __forceinline__ void dequant(const uint4 (&code)[4], const uint32_t (&sc)[Row<D, SF>::SW], int rmax, int p,
-                                        int j, uint8_t *part) {
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {  // 32 channels: half a slice
-        uint8_t *to = part + (v >> 1) * Cfg<D>::SLICE + (j >> 3) * 1024 + (j & 7) * 128;
-        __half2 s2[2];
-        if constexpr (SF == kScaleE8M0x32) {
-            const int k = (int)((sc[p] >> (8 * v)) & 0xFF) - rmax;  // <= 0
-            // 2^k in fp16: normal for k >= -14, subnormal down to -24, else 0
-            const uint16_t hb = k >= -14 ? (uint16_t)((k + 15) << 10) : k >= -24 ? (uint16_t)(1u << (k + 24)) : 0;
-            s2[0] = s2[1] = __halves2half2(__ushort_as_half(hb), __ushort_as_half(hb));
-        } else {
-            // E' = e 2^-7
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t byte = (sc[2 * p + (v >> 1)] >> (8 * (2 * (v & 1) + h))) & 0xFF;
-                const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
-                const __half s = __hmul(__half(hr), __ushort_as_half((uint16_t)((15 - 7) << 10)));
-                s2[h] = __halves2half2(s, s);
-            }
+        for (int b = 0; b < 4; ++b) {
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[b]), s2[k >> 1]);
+            o[b] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        const uint32_t w[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t o[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w[k] >> (8 * b)) & 0xFF), __NV_E2M1);
-                const __half2 h = __hmul2(*reinterpret_cast<__half2 *>(&hr), s2[k >> 1]);
-                o[b] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            *reinterpret_cast<uint4 *>(to + (((4 * (v & 1) + k) ^ (j & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + off[k]), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                     : "memory");
     }
 }
 
@@ -360,10 +351,10 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, ui
 }
 
 // B + 127 from what the dequantizing warps found (E8M0).
-__device__ __forceinline__ int base_of(const int (&b)[kDequantWarps]) {
+__device__ __forceinline__ int base_of(const int (&b)[kTeamWarps]) {
     int m = b[0];
 #pragma unroll
-    for (int k = 1; k < kDequantWarps; ++k) m = max(m, b[k]);
+    for (int k = 1; k < kTeamWarps; ++k) m = max(m, b[k]);
     return m > 0 ? m : 127;
 }
 
@@ -420,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     if (tid == 0) {
         for (int b = 0; b < C::NBUF; ++b)
             for (int p = 0; p < C::PARTS; ++p) {
-                mbar_init(smem_u32(&ms->e_full[b][p]), kDequantWarps);
+                mbar_init(smem_u32(&ms->e_full[b][p]), kTeamWarps);
                 mbar_init(smem_u32(&ms->e_free[b][p]), 1);
             }
         for (int b = 0; b < 2; ++b) {
@@ -431,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             mbar_init(smem_u32(&ms->o_free[b]), kSoftmaxWarps);
         }
         mbar_init(smem_u32(&ms->q_full), kDequantWarps);
-        mbar_init(smem_u32(&ms->r_full), kDequantWarps);
+        mbar_init(smem_u32(&ms->r_full), kTeamWarps);
         mbar_init(smem_u32(&ms->q_free), 1);
         mbar_init(smem_u32(&ms->drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -484,20 +475,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         // nothing to do: fall through to the common end
     } else if (warp < kSoftmaxWarps) {
         // ================================================================ softmax and output
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int j = tid & (kTile - 1), hf = tid >> 7;
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_addr = tmem + lane_off + 32 * hf;
         const uint32_t o_addr = tmem + lane_off + C::TMEM_O + 32 * hf;
-        float lsum[32];
+        const uint32_t l_addr = o_addr + C::PARTS * kCols;  // the row sums lie behind O^T
         int n = 0;  // tiles done by this CTA
         Cursor c = start();
         while (c.left > 0) {
             const Group gr = a.groups[c.g];
             const int seg = c.seg, mp = seg & 1, lt0 = c.lt;
             bool gave_up = false;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) lsum[k] = 0.f;
             while (true) {
                 const bool first = c.first;
                 const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
@@ -565,23 +553,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     if (!first) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int dt = 0; dt < 2 * C::PARTS; ++dt) {
+                        for (int x = 0; x < 2 * (C::PARTS + 1); ++x) {  // O^T, and the row sums behind it
                             float o[16];
-                            const uint32_t at = o_addr + kCols * (dt >> 1) + 16 * (dt & 1);
+                            const uint32_t at = o_addr + kCols * (x >> 1) + 16 * (x & 1);
                             tmem_ld16(at, o);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] *= ms->alpha[32 * hf + 16 * (dt & 1) + k];
+                            for (int k = 0; k < 16; ++k) o[k] *= ms->alpha[32 * hf + 16 * (x & 1) + k];
                             tmem_st16(at, o);
                         }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) lsum[k] *= ms->alpha[32 * hf + k];
                     }
                 }
                 if (gave_up) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[sb]));
-                // P' = 2^(u - rho), fp16, and the row sums (without 2^R, which P' carries for E')
+                // P' = 2^(u - rho), fp16
                 uint8_t *Pn = P + (n % C::NP) * C::P_BYTES + (j >> 3) * 1024 + (j & 7) * 128;
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
@@ -589,12 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
 #pragma unroll
                     for (int q2 = 0; q2 < 4; ++q2) {
                         const int k = 8 * cc + 2 * q2;
-                        const float2 pp = make_float2(pow2(u[k]), pow2(u[k + 1]));
-                        const __half2 hh = __floats2half2_rn(pp.x, pp.y);
+                        u[k] = pow2(u[k]);
+                        u[k + 1] = pow2(u[k + 1]);
+                        const __half2 hh = __floats2half2_rn(u[k], u[k + 1]);
                         pk[q2] = *reinterpret_cast<const uint32_t *>(&hh);
-                        const float2 sum = fma2(pp, rinv, make_float2(lsum[k], lsum[k + 1]));
-                        lsum[k] = sum.x;
-                        lsum[k + 1] = sum.y;
                     }
                     *reinterpret_cast<uint4 *>(Pn + (((4 * hf + cc) ^ (j & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
@@ -602,6 +586,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[n % C::NP]));
+                // the row sums (without 2^R, which P' carries for E'), while the O^T product runs
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float l[16];
+                    if (!first) {
+                        tmem_ld16(l_addr + 16 * x, l);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) l[k] = 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const float2 sum = fma2(make_float2(u[16 * x + k], u[16 * x + k + 1]), rinv, make_float2(l[k], l[k + 1]));
+                        l[k] = sum.x;
+                        l[k + 1] = sum.y;
+                    }
+                    tmem_st16(l_addr + 16 * x, l);
+                }
                 ++n;
                 const bool last = c.mine == 1;
                 step(c);
@@ -609,8 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
             if (gave_up) break;
             // ---------------- the group's output, or its partial
-            transpose_reduce32<false>(lsum);
-            ms->wred[warp & 3][32 * hf + lane] = lsum[0];
+            {
+                float l[32];
+                tmem_ld32(l_addr, l);
+                transpose_reduce32<false>(l);
+                ms->wred[warp & 3][32 * hf + lane] = l[0];
+            }
             const bool ok = wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
             if (bar_or_n<kSoftmaxThreads>(!ok)) {
                 ms->abort = 1;
@@ -649,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[seg & 1]));
                 }
-                const int ch = channel_of(128 * dt + 32 * (warp & 3) + lane);
+                const int ch = 128 * dt + 32 * (warp & 3) + lane;
                 if (!whole) {
                     float *dst = a.part_o + ((size_t)slot * kCols + 32 * hf) * D + ch;
 #pragma unroll
@@ -681,23 +687,51 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         }
     } else if (warp < kMmaWarp) {
         // ================================================================ dequantization, queries
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDequantRegs));
-        const int j = tid - kSoftmaxThreads, dw = warp - kSoftmaxWarps;
-        Row<D, SF> r;
+        // Two teams of four warps take the parts of the tile list in turn (D = 512: parts 0, 2 and 1, 3 of
+        // every tile; D = 128: every other tile).
+        const int dw = warp & 3, team = (warp - kSoftmaxWarps) >> 2, v = lane & 3, rl = lane >> 2;
+        // this lane's rows of a tile are 32 dw + rl + 8 i, i = 0 .. 3
+        const int j = 32 * dw + rl;
+        uint32_t off[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            off[k] = (v >> 1) * C::SLICE + dw * 4096 + rl * 128 + (((4 * (v & 1) + (k ^ (v & 2))) ^ rl) << 4);
+        const uint32_t E_s = smem_u32(E);
         Cursor c = start();
         int slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;
-        // the row this thread dequantizes in a tile of a group, or -1
-        auto row_of = [&](int b, int most, int lt) -> long long {
+        uint4 code[4], ncode[4];
+        Scales sc[4], nsc[4];
+        // rows behind the last visible block are zero codes
+        auto load_codes = [&](uint4 (&to)[4], int b, int most, int lt, int p) {
             const int e = lt * kTile + j;
-            return e < most ? (long long)b * a.cap + e : -1;
+            const uint8_t *src = a.fp4 + ((size_t)b * a.cap + e) * (D / 2) + p * 64 + v * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                to[i] = e + 8 * i < most ? load_here(src + i * 8 * (D / 2)) : make_uint4(0, 0, 0, 0);
+        };
+        auto load_tile_scales = [&](Scales (&to)[4], int b, int most, int lt) {
+            const int e = lt * kTile + j;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                to[i].x = to[i].y = 0;
+                if (e + 8 * i < most) to[i] = load_scales<D, SF>(a, (size_t)b * a.cap + e + 8 * i, v);
+            }
+        };
+        int slot_g = c.g;  // the group that slot and n_max belong to
+        auto source = [&](const Cursor &x) {
+            if (x.g != slot_g) {
+                slot_g = x.g;
+                slot = a.groups[slot_g].b;
+                n_max = a.groups[slot_g].n_max;
+            }
         };
         {
-            const long long row = row_of(slot, n_max, c.lt);
-            r.valid = row >= 0;
-            if (r.valid) {
-                load_scales<D, SF>(a, row, r);
-#pragma unroll
-                for (int p = 0; p < C::PARTS; ++p) load_codes<D, SF>(a, row, p, r);
+            Cursor x = c;
+            if (D == 128 && team == 1) step(x);
+            if (x.left > 0) {
+                source(x);
+                load_codes(code, slot, n_max, x.lt, D == 512 ? team : 0);
+                load_tile_scales(sc, slot, n_max, x.lt);
             }
         }
         int n = 0, base = 127 + 7;
@@ -711,10 +745,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const int cols = gr.nq * a.H, mp = c.seg & 1;
                 if constexpr (SF == kScaleE8M0x32) {  // B, from the rows of the group's first tile
-                    const int mine = __reduce_max_sync(0xffffffffu, r.valid ? row_exponent(r.sc) : 0);
-                    if (lane == 0) {
-                        ms->base[mp][dw] = mine;
-                        mbar_arrive(smem_u32(&ms->r_full));
+                    if (team == (D == 512 ? 0 : n & 1)) {
+                        int mine = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mine = max(mine, row_exponent(sc[i].x));
+                        mine = __reduce_max_sync(0xffffffffu, mine);
+                        if (lane == 0) {
+                            ms->base[mp][dw] = mine;
+                            mbar_arrive(smem_u32(&ms->r_full));
+                        }
                     }
                     ok = wait(&ms->r_full, c.seg & 1, abort);
                     if (!__all_sync(0xffffffffu, ok)) break;
@@ -729,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     uint4 v[2][CH];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int col = dw * (kCols / kDequantWarps) + k0 + x * PER + sub;
+                        const int col = (warp - kSoftmaxWarps) * (kCols / kDequantWarps) + k0 + x * PER + sub;
                         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((size_t)gr.q0 * a.H + col) * D);
 #pragma unroll
                         for (int y = 0; y < CH; ++y)
@@ -737,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     }
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int col = dw * (kCols / kDequantWarps) + k0 + x * PER + sub;
+                        const int col = (warp - kSoftmaxWarps) * (kCols / kDequantWarps) + k0 + x * PER + sub;
                         // max |q| as the largest bit pattern (bf16 magnitudes order like integers)
                         uint32_t mx = 0;
 #pragma unroll
@@ -775,41 +814,75 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
             }
-            // the tile after this one, whose rows are loaded as this one's registers empty
             Cursor nx = c;
             step(nx);
-            if (nx.left > 0 && nx.first) {
-                slot = a.groups[nx.g].b;
-                n_max = a.groups[nx.g].n_max;
-            }
-            const long long row_n = nx.left > 0 ? row_of(slot, n_max, nx.lt) : -1;
-
             const int buf = n % C::NBUF, use = n / C::NBUF;
-            uint8_t *En = E + buf * C::E_BYTES;
-            const bool valid = r.valid;
-            const int rmax = SF == kScaleE8M0x32 && valid ? max(row_exponent(r.sc), base - kExponentSpan) : base;
-            // (a part at a time, without leaving the loop early, so that the codes stay in registers)
+            // one part: the next one's codes on their way, this one's into its place in shared memory
+            auto rows_to = [&](int p, const int (&rmax)[4]) {
+                if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                if (p == 0 && v == 0)
 #pragma unroll
-            for (int p = 0; p < C::PARTS; ++p) {
-                if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort) && ok;
-                if (p == 0) ms->rexp[buf][j] = (float)(rmax - base);
-                uint8_t *to = En + 2 * p * C::SLICE;
-                if (valid) {
-                    dequant<D, SF>(r.code[p], r.sc, rmax, p, j, to);
-                } else {
+                    for (int i = 0; i < 4; ++i) ms->rexp[buf][j + 8 * i] = (float)(rmax[i] - base);
+                const uint32_t to = E_s + buf * C::E_BYTES + p * (2 * C::SLICE);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        *reinterpret_cast<uint4 *>(to + (k >> 3) * C::SLICE + (j >> 3) * 1024 + (j & 7) * 128 +
-                                                   ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    Scales s = sc[i];
+                    if constexpr (D == 512) {  // part p's words are lane p's of the four
+                        s.x = __shfl_sync(0xffffffffu, s.x, (lane & ~3) | p);
+                        if constexpr (SF == kScaleE4M3x16) s.y = __shfl_sync(0xffffffffu, s.y, (lane & ~3) | p);
+                    }
+                    dequant<SF>(code[i], s, rmax[i], v, off, to + i * 1024);
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->e_full[buf][p]));
-                if (row_n >= 0) load_codes<D, SF>(a, row_n, p, r);  // (this part's registers are free)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) code[i] = ncode[i];
+            };
+            auto exponents = [&](int (&rmax)[4], int most) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    rmax[i] = base;
+                    if constexpr (SF == kScaleE8M0x32) {
+                        const int m = row_exponent(sc[i].x);
+                        rmax[i] = c.lt * kTile + j + 8 * i < most ? max(m, base - kExponentSpan) : base;
+                    }
+                }
+            };
+            if constexpr (D == 512) {
+                const int this_slot = slot, this_max = n_max;
+                int rmax[4];
+                exponents(rmax, this_max);
+                if (nx.left > 0) {
+                    source(nx);
+                    load_tile_scales(nsc, slot, n_max, nx.lt);
+                }
+#pragma unroll 1
+                for (int p = team; p < C::PARTS && ok; p += 2) {
+                    if (p + 2 < C::PARTS) load_codes(ncode, this_slot, this_max, c.lt, p + 2);
+                    else if (nx.left > 0) load_codes(ncode, slot, n_max, nx.lt, team);
+                    rows_to(p, rmax);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
+            } else if ((n & 1) == team) {
+                Cursor n2 = nx;
+                if (nx.left > 0) step(n2);
+                int rmax[4];
+                exponents(rmax, n_max);
+                if (n2.left > 0) {
+                    source(n2);
+                    load_tile_scales(nsc, slot, n_max, n2.lt);
+                    load_codes(ncode, slot, n_max, n2.lt, 0);
+                }
+                rows_to(0, rmax);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
             }
-            if (!__all_sync(0xffffffffu, ok)) break;
-            r.valid = row_n >= 0;
-            if (r.valid) load_scales<D, SF>(a, row_n, r);
             ++n;
             c = nx;
         }
