@@ -51,9 +51,11 @@ constexpr int kThreads = 32 * (kSoftmaxWarps + kDequantWarps + 1);
 constexpr int kTeamWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 // Row exponents count from B, the largest of the group's first tile in the CTA (127, that is 1, when
-// its rows are all zero), and a row's is at least B - 40: what that flushes to zero lies below
-// 2^-64 of the first tile's scale, and no sum leaves float32's range over all-zero rows (scale byte 0)
-constexpr int kExponentSpan = 40;
+// its rows are all zero). fp16 holds a row of 2^(B - 10) .. 2^(B + 12) exactly without an exponent of its own
+// (groups down to 2^-13 of the row's largest, which a row at B has down to 2^-23), and then takes none: R = 0. Others
+// take theirs, but at least B - 40: what that flushes to zero lies below 2^-64 of the first tile's scale,
+// and no sum leaves float32's range over all-zero rows (scale byte 0).
+constexpr int kExponentSpan = 40, kEvenBelow = 10, kEvenAbove = 12;
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
@@ -68,8 +70,8 @@ struct Cfg {
     static constexpr int P_BYTES = kTile * kCols * 2;
     static constexpr int SLICE = kTile * 128;            // 64 channels of a tile
     static constexpr int QSLICE = kCols * 128;           // 64 channels of the queries
-    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T, then the row sums
-    static constexpr int TMEM_COLS = TMEM_O + (PARTS + 1) * kCols <= 256 ? 256 : 512;
+    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T
+    static constexpr int TMEM_COLS = TMEM_O + PARTS * kCols <= 256 ? 256 : 512;
     static constexpr int MISC = 6144;
     static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
 };
@@ -244,42 +246,49 @@ __device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&o)[4]) {
         : "r"(w));
 }
 
-// This lane's 32 channels of one part of a row, as fp16 into its 128-byte-swizzled place: four 16-byte stores, the
-// second slice's in another order than the first's so that eight lanes meet eight banks. to: the row's
-// place in this lane's slice, off: the four offsets.
-template <int SF>
-__device__ __forceinline__ void dequant(const uint4 &code, Scales sc, int rmax, int v, const uint32_t (&off)[4],
-                                        uint32_t to) {
-    __half2 s2[2];
-    const bool second = (v & 2) != 0;
+// Where a part's 16 chunks of 8 channels go: chunk 4 v + k (lane v's word k) becomes chunk 8 (k / 2) + 2 v + k % 2, so
+// that for every k the eight lanes of two rows store to eight different banks. Queries follow in the
+// same order, and outputs are read back through channel_at.
+__device__ __forceinline__ int chunk_place(int kc) { return 8 * ((kc >> 1) & 1) + 2 * (kc >> 2) + (kc & 1); }
+__device__ __forceinline__ int channel_at(int pos) {  // of a part's position
+    const int pc = pos >> 3;
+    return 8 * (4 * ((pc & 7) >> 1) + 2 * (pc >> 3) + (pc & 1)) + (pos & 7);
+}
+
+// This lane's 32 channels of one part of row 32 dw + rl + 8 I, as fp16 into its 128-byte-swizzled place. to0, to1: the
+// places of words 0 and 1 of row 32 dw + rl; words 2 and 3 lie a slice further on.
+template <int SF, int I, int SLICE>
+__device__ __forceinline__ void dequant(const uint4 &code, Scales sc, int rmax, int v, uint32_t to0, uint32_t to1) {
+    uint32_t s2[2];
     if constexpr (SF == kScaleE8M0x32) {
-        const int k = (int)((sc.x >> (8 * v)) & 0xFF) - rmax;  // <= 0
-        // 2^k in fp16: normal for k >= -14, subnormal down to -24, else 0
-        const uint32_t hb = k >= -14 ? (uint32_t)(k + 15) << 10 : k >= -24 ? 1u << (k + 24) : 0u;
-        const uint32_t h2 = hb * 0x10001u;
-        s2[0] = s2[1] = *reinterpret_cast<const __half2 *>(&h2);
+        // 2^(X - rmax) from a float32 with that exponent (fp16 rounds what lies below 2^-25 to zero)
+        const int e = max((int)((sc.x >> (8 * v)) & 0xFF) - rmax + 127, 0);
+        const float f = __uint_as_float((uint32_t)e << 23);
+        const __half2 h = __floats2half2_rn(f, f);
+        s2[0] = s2[1] = *reinterpret_cast<const uint32_t *>(&h);
     } else {
         // E' = e 2^-7
-        const uint32_t bytes = (second ? sc.y : sc.x) >> (16 * (v & 1));
+        const uint32_t bytes = ((v & 2) ? sc.y : sc.x) >> (16 * (v & 1));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)((bytes >> (8 * (second ? 1 - h : h))) & 0xFF), __NV_E4M3);
-            const __half s = __hmul(__half(hr), __ushort_as_half((uint16_t)((15 - 7) << 10)));
-            s2[h] = __halves2half2(s, s);
+            const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)((bytes >> (8 * h)) & 0xFF), __NV_E4M3);
+            const __half x = __hmul(__half(hr), __ushort_as_half((uint16_t)((15 - 7) << 10)));
+            const __half2 x2 = __halves2half2(x, x);
+            s2[h] = *reinterpret_cast<const uint32_t *>(&x2);
         }
     }
-    const uint32_t w[4] = {second ? code.z : code.x, second ? code.w : code.y, second ? code.x : code.z,
-                           second ? code.y : code.w};
+    const uint32_t w[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         uint32_t o[4];
         e2m1_halves(w[k], o);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[b]), s2[k >> 1]);
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[b]), *reinterpret_cast<const __half2 *>(&s2[k >> 1]));
             o[b] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + off[k]), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(((k & 1) ? to1 : to0) + I * 1024 + (k >> 1) * SLICE),
+                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                      : "memory");
     }
 }
@@ -350,6 +359,41 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, ui
         : "memory");
 }
 
+// Sixteen rows by 64 columns of TMEM (fragment of m8n8 matrices): v[4 b + e] is row lane / 4, v[4 b + 2 + e] row
+// lane / 4 + 8, of column 8 b + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+// Reduction over the eight lanes with the same lane % 4 (its column pairs v[b], b = 0 .. 7): afterwards v[0] of lane
+// L is the pair b = L / 4, columns 2 L and 2 L + 1 of the 64.
+template <bool MAX>
+__device__ __forceinline__ void reduce_columns(float2 (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int half = 4; half >= 1; half >>= 1) {
+        const bool hi = (lane & (4 * half)) != 0;
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const float2 send = hi ? v[k] : v[k + half], keep = hi ? v[k + half] : v[k];
+            const float gx = __shfl_xor_sync(0xffffffffu, send.x, 4 * half);
+            const float gy = __shfl_xor_sync(0xffffffffu, send.y, 4 * half);
+            v[k] = MAX ? make_float2(fmaxf(keep.x, gx), fmaxf(keep.y, gy)) : make_float2(keep.x + gx, keep.y + gy);
+        }
+    }
+}
+
 // B + 127 from what the dequantizing warps found (E8M0).
 __device__ __forceinline__ int base_of(const int (&b)[kTeamWarps]) {
     int m = b[0];
@@ -390,7 +434,7 @@ struct Misc {
     uint32_t tmem;
     int abort;
     alignas(16) float minus_rho[kCols], alpha[kCols], fac[kCols], jfac[kCols];
-    float wred[4][kCols];
+    float wred[kSoftmaxWarps][kCols];
     float colmul[2][kCols];  // scale_log2 * 2^(sQ + B) of each column, by segment parity
     int nvis[2][kCols];
     float rexp[3][kTile];    // R_j - B
@@ -475,17 +519,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         // nothing to do: fall through to the common end
     } else if (warp < kSoftmaxWarps) {
         // ================================================================ softmax and output
-        const int j = tid & (kTile - 1), hf = tid >> 7;
+        // S^T: 16 rows (blocks) a warp, and of them two a thread, in all 64 columns of which a thread has 16:
+        // rows r0 and r0 + 8, columns 8 b + 2 (lane % 4) + {0, 1}, b = 0 .. 7 (the fragment that 16x256b loads
+        // give and stmatrix takes). A column's factors are so read once for two rows.
+        // O^T: 32 lanes (channels) and 32 columns a warp, one channel a thread.
+        const int hf = tid >> 7, r0 = 32 * (warp & 3) + 16 * hf + (lane >> 2), c0 = 2 * (lane & 3);
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_addr = tmem + lane_off + 32 * hf;
+        const uint32_t s_addr = tmem + lane_off + ((uint32_t)(16 * hf) << 16);
         const uint32_t o_addr = tmem + lane_off + C::TMEM_O + 32 * hf;
-        const uint32_t l_addr = o_addr + C::PARTS * kCols;  // the row sums lie behind O^T
-        int n = 0;  // tiles done by this CTA
+        // stmatrix: lanes 8 i .. 8 i + 7 address matrix i = (rows 0-7 | 8-15) of column blocks b and b + 1
+        const uint32_t p_addr = smem_u32(P) + (4 * (warp & 3) + 2 * hf + ((lane >> 3) & 1)) * 1024 + (lane & 7) * 128 +
+                                (((lane >> 4) ^ (lane & 7)) << 4);
+        float2 lsum[8];  // sums of this thread's columns over its rows
+        int n = 0;       // tiles done by this CTA
         Cursor c = start();
         while (c.left > 0) {
             const Group gr = a.groups[c.g];
             const int seg = c.seg, mp = seg & 1, lt0 = c.lt;
             bool gave_up = false;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) lsum[b] = make_float2(0.f, 0.f);
             while (true) {
                 const bool first = c.first;
                 const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
@@ -493,57 +546,80 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 if (n >= C::NP)  // P' is free: the O^T product of tile n - NP is done
                     ok = wait(&ms->pv_done[(n - C::NP) & 1], ((n - C::NP) >> 1) & 1, abort);
                 ok = ok && wait(&ms->e_full[buf][0], use & 1, abort);
-                const float R = ms->rexp[buf][j];  // the row's exponent from B on
-                const float rmul = pow2(R);
-                const float2 rinv = make_float2(pow2(-R), pow2(-R));
+                // the rows' exponents from B on: 0 for almost all of them
+                const float R0 = ms->rexp[buf][r0], R1 = ms->rexp[buf][r0 + 8];
+                const bool even = !__any_sync(0xffffffffu, R0 != 0.f || R1 != 0.f);
+                const bool masked = (c.lt + 1) * kTile > gr.n_min;
                 ok = ok && wait(&ms->s_full[sb], (n >> 1) & 1, abort);
                 tc_fence_after();
-                const int entry = c.lt * kTile + j;
-                const bool masked = entry - j + kTile > gr.n_min;
                 float u[32];
-                // u + R - rho of this thread's 32 columns. References are set by the group's first tile, and
+                // u + R - rho of this thread's rows and columns. References are set by the group's first tile, and
                 // raised (with O^T and the sums) when a logit exceeds one by more than 8: then once more from
                 // the start, with the new ones. (A second raise happens only where a logit is so large that
-                // the first one was rounded.) A wait that ran out comes this way too.
+                // the first one was rounded; what rounding then leaves above is cut.) A wait that ran out
+                // comes this way too.
                 for (int pass = 0;; ++pass) {
                     float over = -INFINITY;
-                    tmem_ld32(s_addr + kCols * sb, u);
+                    tmem_ld_rows(s_addr + kCols * sb, u);
+                    if (even) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 cm = *reinterpret_cast<const float4 *>(&ms->colmul[mp][32 * hf + k]);
-                        const float4 rh = *reinterpret_cast<const float4 *>(&ms->minus_rho[32 * hf + k]);
-                        const float2 rm = make_float2(rmul, rmul), r2 = make_float2(R, R);
-                        // (two roundings, so that the entry that set a reference is at 0 exactly)
-                        const float2 x = add2(fma2(make_float2(u[k], u[k + 1]), mul2(make_float2(cm.x, cm.y), rm), r2),
-                                              make_float2(rh.x, rh.y));
-                        const float2 y = add2(fma2(make_float2(u[k + 2], u[k + 3]), mul2(make_float2(cm.z, cm.w), rm), r2),
-                                              make_float2(rh.z, rh.w));
-                        u[k] = x.x;
-                        u[k + 1] = x.y;
-                        u[k + 2] = y.x;
-                        u[k + 3] = y.y;
-                        if (masked) {
-                            const int4 nv = *reinterpret_cast<const int4 *>(&ms->nvis[mp][32 * hf + k]);
-                            if (entry >= nv.x) u[k] = -INFINITY;
-                            if (entry >= nv.y) u[k + 1] = -INFINITY;
-                            if (entry >= nv.z) u[k + 2] = -INFINITY;
-                            if (entry >= nv.w) u[k + 3] = -INFINITY;
+                        for (int b = 0; b < 8; ++b) {
+                            const float2 cm = *reinterpret_cast<const float2 *>(&ms->colmul[mp][8 * b + c0]);
+                            const float2 rh = *reinterpret_cast<const float2 *>(&ms->minus_rho[8 * b + c0]);
+                            const float2 x = fma2(make_float2(u[4 * b], u[4 * b + 1]), cm, rh);
+                            const float2 y = fma2(make_float2(u[4 * b + 2], u[4 * b + 3]), cm, rh);
+                            u[4 * b] = x.x;
+                            u[4 * b + 1] = x.y;
+                            u[4 * b + 2] = y.x;
+                            u[4 * b + 3] = y.y;
                         }
-                        over = fmaxf(over, fmaxf(fmaxf(u[k], u[k + 1]), fmaxf(u[k + 2], u[k + 3])));
+                    } else {
+                        const float m0 = pow2(R0), m1 = pow2(R1);
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const float2 cm = *reinterpret_cast<const float2 *>(&ms->colmul[mp][8 * b + c0]);
+                            const float2 rh = *reinterpret_cast<const float2 *>(&ms->minus_rho[8 * b + c0]);
+                            u[4 * b] = fmaf(u[4 * b], cm.x * m0, rh.x + R0);
+                            u[4 * b + 1] = fmaf(u[4 * b + 1], cm.y * m0, rh.y + R0);
+                            u[4 * b + 2] = fmaf(u[4 * b + 2], cm.x * m1, rh.x + R1);
+                            u[4 * b + 3] = fmaf(u[4 * b + 3], cm.y * m1, rh.y + R1);
+                        }
                     }
+                    if (masked) {
+                        const int e0 = c.lt * kTile + r0;
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const int2 nv = *reinterpret_cast<const int2 *>(&ms->nvis[mp][8 * b + c0]);
+                            if (e0 >= nv.x) u[4 * b] = -INFINITY;
+                            if (e0 >= nv.y) u[4 * b + 1] = -INFINITY;
+                            if (e0 + 8 >= nv.x) u[4 * b + 2] = -INFINITY;
+                            if (e0 + 8 >= nv.y) u[4 * b + 3] = -INFINITY;
+                        }
+                    }
+                    if (pass >= 2) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) u[k] = u[k] > 8.f ? 8.f : u[k];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) over = fmaxf(over, u[k]);
                     const bool set = first && pass == 0;
-                    if (!bar_or_n<kSoftmaxThreads>(set || over > 8.f || !ok) || pass == 4) break;
+                    if (!bar_or_n<kSoftmaxThreads>(set || over > 8.f || !ok)) break;
                     if (!first) ok = ok && wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
-                    transpose_reduce32<true>(u);  // lane L: column 32 hf + L over this warp's entries
-                    ms->wred[warp & 3][32 * hf + lane] = u[0];
+                    float2 m[8];
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        m[b] = make_float2(fmaxf(u[4 * b], u[4 * b + 2]), fmaxf(u[4 * b + 1], u[4 * b + 3]));
+                    reduce_columns<true>(m);  // lane L: columns 2 L and 2 L + 1
+                    *reinterpret_cast<float2 *>(&ms->wred[warp][2 * lane]) = m[0];
                     if (bar_or_n<kSoftmaxThreads>(!ok)) {
                         ms->abort = 1;
                         gave_up = true;
                         break;
                     }
                     if (tid < kCols) {
-                        const float M = fmaxf(fmaxf(ms->wred[0][tid], ms->wred[1][tid]),
-                                              fmaxf(ms->wred[2][tid], ms->wred[3][tid]));
+                        float M = ms->wred[0][tid];
+#pragma unroll
+                        for (int w = 1; w < kSoftmaxWarps; ++w) M = fmaxf(M, ms->wred[w][tid]);
                         // (a column that sees nothing of its first tile sees nothing of the others)
                         const bool raise = set ? M > -INFINITY : M > 8.f;
                         if (raise) ms->minus_rho[tid] -= M;
@@ -553,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     if (!first) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int x = 0; x < 2 * (C::PARTS + 1); ++x) {  // O^T, and the row sums behind it
+                        for (int x = 0; x < 2 * C::PARTS; ++x) {
                             float o[16];
                             const uint32_t at = o_addr + kCols * (x >> 1) + 16 * (x & 1);
                             tmem_ld16(at, o);
@@ -561,6 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                             for (int k = 0; k < 16; ++k) o[k] *= ms->alpha[32 * hf + 16 * (x & 1) + k];
                             tmem_st16(at, o);
                         }
+#pragma unroll
+                        for (int b = 0; b < 8; ++b)
+                            lsum[b] = mul2(lsum[b], *reinterpret_cast<const float2 *>(&ms->alpha[8 * b + c0]));
                     }
                 }
                 if (gave_up) break;
@@ -568,41 +647,37 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[sb]));
                 // P' = 2^(u - rho), fp16
-                uint8_t *Pn = P + (n % C::NP) * C::P_BYTES + (j >> 3) * 1024 + (j & 7) * 128;
+                const uint32_t Pn = p_addr + (n % C::NP) * C::P_BYTES;
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
+                for (int b = 0; b < 8; b += 2) {
                     uint32_t pk[4];
 #pragma unroll
-                    for (int q2 = 0; q2 < 4; ++q2) {
-                        const int k = 8 * cc + 2 * q2;
+                    for (int q = 0; q < 4; ++q) {
+                        const int k = 4 * b + 2 * q;
                         u[k] = pow2(u[k]);
                         u[k + 1] = pow2(u[k + 1]);
                         const __half2 hh = __floats2half2_rn(u[k], u[k + 1]);
-                        pk[q2] = *reinterpret_cast<const uint32_t *>(&hh);
+                        pk[q] = *reinterpret_cast<const uint32_t *>(&hh);
                     }
-                    *reinterpret_cast<uint4 *>(Pn + (((4 * hf + cc) ^ (j & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(Pn ^ (b << 4)),
+                                 "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                                 : "memory");
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[n % C::NP]));
-                // the row sums (without 2^R, which P' carries for E'), while the O^T product runs
+                // the sums (without 2^R, which P' carries for E'), while the O^T product runs
+                if (even) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float l[16];
-                    if (!first) {
-                        tmem_ld16(l_addr + 16 * x, l);
-                    } else {
+                    for (int b = 0; b < 8; ++b)
+                        lsum[b] = add2(lsum[b], add2(make_float2(u[4 * b], u[4 * b + 1]), make_float2(u[4 * b + 2], u[4 * b + 3])));
+                } else {
+                    const float2 i0 = make_float2(pow2(-R0), pow2(-R0)), i1 = make_float2(pow2(-R1), pow2(-R1));
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) l[k] = 0.f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        const float2 sum = fma2(make_float2(u[16 * x + k], u[16 * x + k + 1]), rinv, make_float2(l[k], l[k + 1]));
-                        l[k] = sum.x;
-                        l[k + 1] = sum.y;
-                    }
-                    tmem_st16(l_addr + 16 * x, l);
+                    for (int b = 0; b < 8; ++b)
+                        lsum[b] = fma2(make_float2(u[4 * b], u[4 * b + 1]), i0,
+                                       fma2(make_float2(u[4 * b + 2], u[4 * b + 3]), i1, lsum[b]));
                 }
                 ++n;
                 const bool last = c.mine == 1;
@@ -611,12 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
             if (gave_up) break;
             // ---------------- the group's output, or its partial
-            {
-                float l[32];
-                tmem_ld32(l_addr, l);
-                transpose_reduce32<false>(l);
-                ms->wred[warp & 3][32 * hf + lane] = l[0];
-            }
+            reduce_columns<false>(lsum);
+            *reinterpret_cast<float2 *>(&ms->wred[warp][2 * lane]) = lsum[0];
             const bool ok = wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
             if (bar_or_n<kSoftmaxThreads>(!ok)) {
                 ms->abort = 1;
@@ -629,7 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             const float unit = SF == kScaleE8M0x32 ? exp2f((float)(base_of(ms->base[mp]) - 127)) : exp2f(7.f);
             const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
             if (tid < kCols) {
-                const float l = ms->wred[0][tid] + ms->wred[1][tid] + ms->wred[2][tid] + ms->wred[3][tid];
+                float l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kSoftmaxWarps; ++w) l += ms->wred[w][tid];
                 const float rho = -ms->minus_rho[tid];
                 if (!whole) {
                     a.part_rho[(size_t)slot * kCols + tid] = l == 0.f ? -INFINITY : rho;
@@ -655,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[seg & 1]));
                 }
-                const int ch = 128 * dt + 32 * (warp & 3) + lane;
+                const int ch = 128 * dt + channel_at(32 * (warp & 3) + lane);
                 if (!whole) {
                     float *dst = a.part_o + ((size_t)slot * kCols + 32 * hf) * D + ch;
 #pragma unroll
@@ -692,46 +765,55 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         const int dw = warp & 3, team = (warp - kSoftmaxWarps) >> 2, v = lane & 3, rl = lane >> 2;
         // this lane's rows of a tile are 32 dw + rl + 8 i, i = 0 .. 3
         const int j = 32 * dw + rl;
-        uint32_t off[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            off[k] = (v >> 1) * C::SLICE + dw * 4096 + rl * 128 + (((4 * (v & 1) + (k ^ (v & 2))) ^ rl) << 4);
-        const uint32_t E_s = smem_u32(E);
+        const uint32_t place = smem_u32(E) + dw * 4096 + rl * 128;
+        const uint32_t off0 = place + (((2 * v) ^ rl) << 4), off1 = place + (((2 * v + 1) ^ rl) << 4);
+        // the parts of a tile that this lane's registers hold: team, team + 2 (D = 512)
+        constexpr int MINE = D == 512 ? 2 : 1;
         Cursor c = start();
-        int slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;
-        uint4 code[4], ncode[4];
+        int slot_g = c.g, slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;  // the group of the rows asked for last
+        uint4 code[MINE][4];
         Scales sc[4], nsc[4];
-        // rows behind the last visible block are zero codes
-        auto load_codes = [&](uint4 (&to)[4], int b, int most, int lt, int p) {
-            const int e = lt * kTile + j;
-            const uint8_t *src = a.fp4 + ((size_t)b * a.cap + e) * (D / 2) + p * 64 + v * 16;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to[i] = e + 8 * i < most ? load_here(src + i * 8 * (D / 2)) : make_uint4(0, 0, 0, 0);
+        // this lane's first row of a tile (its codes of part 0), and how many rows from there on are visible
+        // (the others are zero codes)
+        struct Rows {
+            const uint8_t *codes;
+            size_t row;
+            int live;
         };
-        auto load_tile_scales = [&](Scales (&to)[4], int b, int most, int lt) {
-            const int e = lt * kTile + j;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                to[i].x = to[i].y = 0;
-                if (e + 8 * i < most) to[i] = load_scales<D, SF>(a, (size_t)b * a.cap + e + 8 * i, v);
-            }
-        };
-        int slot_g = c.g;  // the group that slot and n_max belong to
-        auto source = [&](const Cursor &x) {
+        auto rows_of = [&](const Cursor &x) {
             if (x.g != slot_g) {
                 slot_g = x.g;
                 slot = a.groups[slot_g].b;
                 n_max = a.groups[slot_g].n_max;
             }
+            const int e = x.lt * kTile + j;
+            Rows r;
+            r.row = (size_t)slot * a.cap + e;
+            r.codes = a.fp4 + r.row * (D / 2) + v * 16;
+            r.live = n_max - e;
+            return r;
         };
+        auto load_codes = [&](uint4 (&to)[4], const uint8_t *src, int live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                to[i] = 8 * i < live ? load_here(src + i * 8 * (D / 2)) : make_uint4(0, 0, 0, 0);
+        };
+        auto load_tile_scales = [&](Scales (&to)[4], const Rows &r) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                to[i].x = to[i].y = 0;
+                if (8 * i < r.live) to[i] = load_scales<D, SF>(a, r.row + 8 * i, v);
+            }
+        };
+        Rows rows = {};  // of the tile that code and sc hold
         {
             Cursor x = c;
             if (D == 128 && team == 1) step(x);
             if (x.left > 0) {
-                source(x);
-                load_codes(code, slot, n_max, x.lt, D == 512 ? team : 0);
-                load_tile_scales(sc, slot, n_max, x.lt);
+                rows = rows_of(x);
+#pragma unroll
+                for (int m = 0; m < MINE; ++m) load_codes(code[m], rows.codes + (D == 512 ? (team + 2 * m) * 64 : 0), rows.live);
+                load_tile_scales(sc, rows);
             }
         }
         int n = 0, base = 127 + 7;
@@ -801,8 +883,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                                 const __half2 hh = __floats2half2_rn(f.x * inv, f.y * inv);
                                 o[z] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
-                            *reinterpret_cast<uint4 *>(Q + (kc >> 3) * C::QSLICE + (col >> 3) * 1024 + (col & 7) * 128 +
-                                                       (((kc & 7) ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            const int pc = (kc & ~15) + chunk_place(kc & 15);
+                            *reinterpret_cast<uint4 *>(Q + (pc >> 3) * C::QSLICE + (col >> 3) * 1024 + (col & 7) * 128 +
+                                                       (((pc & 7) ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                         if (sl == 0) {
                             ms->colmul[mp][col] = ldexpf(a.scale_log2, sq + base - 127);
@@ -817,69 +900,65 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             Cursor nx = c;
             step(nx);
             const int buf = n % C::NBUF, use = n / C::NBUF;
-            // one part: the next one's codes on their way, this one's into its place in shared memory
-            auto rows_to = [&](int p, const int (&rmax)[4]) {
-                if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
+            // one part into its place in shared memory, and the same part of this team's next tile on its way
+            auto part = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const Rows &next) {
+                if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort) && ok;
                 if (p == 0 && v == 0)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ms->rexp[buf][j + 8 * i] = (float)(rmax[i] - base);
-                const uint32_t to = E_s + buf * C::E_BYTES + p * (2 * C::SLICE);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    Scales s = sc[i];
+                const uint32_t at = buf * C::E_BYTES + p * (2 * C::SLICE);
+                auto words = [&](int i) {
+                    Scales x = sc[i];
                     if constexpr (D == 512) {  // part p's words are lane p's of the four
-                        s.x = __shfl_sync(0xffffffffu, s.x, (lane & ~3) | p);
-                        if constexpr (SF == kScaleE4M3x16) s.y = __shfl_sync(0xffffffffu, s.y, (lane & ~3) | p);
+                        x.x = __shfl_sync(0xffffffffu, x.x, (lane & ~3) | p);
+                        if constexpr (SF == kScaleE4M3x16) x.y = __shfl_sync(0xffffffffu, x.y, (lane & ~3) | p);
                     }
-                    dequant<SF>(code[i], s, rmax[i], v, off, to + i * 1024);
-                }
+                    return x;
+                };
+                dequant<SF, 0, C::SLICE>(from[0], words(0), rmax[0], v, off0 + at, off1 + at);
+                dequant<SF, 1, C::SLICE>(from[1], words(1), rmax[1], v, off0 + at, off1 + at);
+                dequant<SF, 2, C::SLICE>(from[2], words(2), rmax[2], v, off0 + at, off1 + at);
+                dequant<SF, 3, C::SLICE>(from[3], words(3), rmax[3], v, off0 + at, off1 + at);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->e_full[buf][p]));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) code[i] = ncode[i];
+                load_codes(from, next.codes + p * 64, next.live);
             };
-            auto exponents = [&](int (&rmax)[4], int most) {
+            auto exponents = [&](int (&rmax)[4]) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     rmax[i] = base;
                     if constexpr (SF == kScaleE8M0x32) {
-                        const int m = row_exponent(sc[i].x);
-                        rmax[i] = c.lt * kTile + j + 8 * i < most ? max(m, base - kExponentSpan) : base;
+                        const int m = row_exponent(sc[i].x), d = m - base;
+                        if (8 * i < rows.live && (d < -kEvenBelow || d > kEvenAbove)) rmax[i] = max(m, base - kExponentSpan);
                     }
                 }
             };
             if constexpr (D == 512) {
-                const int this_slot = slot, this_max = n_max;
                 int rmax[4];
-                exponents(rmax, this_max);
+                exponents(rmax);
+                Rows next = {};
                 if (nx.left > 0) {
-                    source(nx);
-                    load_tile_scales(nsc, slot, n_max, nx.lt);
+                    next = rows_of(nx);
+                    load_tile_scales(nsc, next);
                 }
-#pragma unroll 1
-                for (int p = team; p < C::PARTS && ok; p += 2) {
-                    if (p + 2 < C::PARTS) load_codes(ncode, this_slot, this_max, c.lt, p + 2);
-                    else if (nx.left > 0) load_codes(ncode, slot, n_max, nx.lt, team);
-                    rows_to(p, rmax);
-                }
-                if (!ok) break;
+#pragma unroll
+                for (int m = 0; m < MINE; ++m) part(code[m], team + 2 * m, rmax, next);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                rows = next;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
             } else if ((n & 1) == team) {
                 Cursor n2 = nx;
                 if (nx.left > 0) step(n2);
                 int rmax[4];
-                exponents(rmax, n_max);
-                if (n2.left > 0) {
-                    source(n2);
-                    load_tile_scales(nsc, slot, n_max, n2.lt);
-                    load_codes(ncode, slot, n_max, n2.lt, 0);
-                }
-                rows_to(0, rmax);
-                if (!ok) break;
+                exponents(rmax);
+                Rows next = {};
+                if (n2.left > 0) next = rows_of(n2);
+                load_tile_scales(nsc, next);
+                part(code[0], 0, rmax, next);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                rows = next;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
             }
