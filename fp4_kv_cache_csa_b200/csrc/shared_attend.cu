@@ -25,12 +25,20 @@
 //
 // Warp roles (17 warps, one CTA per SM): eight dequantize (they also bring the
 // group's queries in), eight do the softmax and the outputs, one thread issues the
-// MMAs. What bounds it at D = 512: M = 128, N = 64 MMAs read 6 KB of operands from
-// shared memory per 128 x 64 x 16 products, so shared memory (128 B/cycle) holds them to
-// 0.63 of the tensor rate; the 128 KB tile of 128 blocks leaves no room for a second one,
-// so a tile's parts (128 channels each) are replaced as its O^T products release
-// them, and the tensor core waits while the softmax of a tile runs. At D = 128 three
-// tiles fit and the softmax is the bound.
+// MMAs. At D = 512 a tile of E' takes 128 KB of shared memory, which leaves no room for a
+// second one, and O^T needs it as long as its product runs. So S^T of the next tile takes
+// its E' from tensor memory instead: four of the dequantizing warps write it there part
+// by part (128 channels, two buffers), the other four dequantize the same tile again into
+// shared memory as O^T releases its parts; S^T, softmax and O^T of neighbouring tiles then
+// overlap (one tile after the other, converted once: 1.70 ms; this: 1.64 ms at 512 x 64 heads
+// over 16384 blocks). At D = 128 three tiles fit shared memory and both products read them there.
+//
+// What bounds it: an MMA of M = 128, N = 64, K = 16 takes 48 cycles here with A in shared
+// memory (4 KB at about 90 B/cycle; N = 32 takes as long) against 32 at the tensor rate, so O^T
+// and S^T take about 3000 cycles of a tile; 128 x 64 exponentials 512 cycles of the
+// special-function units; and each conversion of the tile about 2000 warp instructions.
+// Measured, a tile of 64 columns takes about 6500 cycles: the conversions' instruction
+// issue bounds it, then the softmax between the two products.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -70,8 +78,11 @@ struct Cfg {
     static constexpr int P_BYTES = kTile * kCols * 2;
     static constexpr int SLICE = kTile * 128;            // 64 channels of a tile
     static constexpr int QSLICE = kCols * 128;           // 64 channels of the queries
-    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T
-    static constexpr int TMEM_COLS = TMEM_O + PARTS * kCols <= 256 ? 256 : 512;
+    // D = 512: the blocks' operand of S^T comes through tensor memory, part by part (see the top)
+    static constexpr bool THROUGH_TMEM = D == 512;
+    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T, then two parts of E'
+    static constexpr int TMEM_E = TMEM_O + PARTS * kCols;
+    static constexpr int TMEM_COLS = TMEM_E + (THROUGH_TMEM ? 2 * kCols : 0) <= 256 ? 256 : 512;
     static constexpr int MISC = 6144;
     static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
 };
@@ -211,20 +222,16 @@ struct Scales {
     uint32_t x, y;
 };
 
-template <int D, int SF>
-__device__ __forceinline__ Scales load_scales(const SharedArgs &a, size_t row, int v) {
-    constexpr int WORDS = SF == kScaleE4M3x16 ? 2 : 1;  // of a part
-    const uint8_t *src = a.scale + row * (4 * WORDS * Cfg<D>::PARTS) + (D == 512 ? 4 * WORDS * v : 0);
-    Scales r;
-    r.x = __ldg(reinterpret_cast<const uint32_t *>(src));
-    r.y = WORDS == 2 ? __ldg(reinterpret_cast<const uint32_t *>(src) + 1) : 0;
-    return r;
-}
-
 // A load that is issued where it stands (left to itself it is moved down to its use, a part later).
 __device__ __forceinline__ uint4 load_here(const uint8_t *p) {
     uint4 r;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t load_word(const uint8_t *p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
     return r;
 }
 
@@ -247,19 +254,17 @@ __device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&o)[4]) {
 }
 
 // Where a part's 16 chunks of 8 channels go: chunk 4 v + k (lane v's word k) becomes chunk 8 (k / 2) + 2 v + k % 2, so
-// that for every k the eight lanes of two rows store to eight different banks. Queries follow in the
-// same order, and outputs are read back through channel_at.
+// that for every k the eight lanes of two rows store to eight different banks. Outputs are read back through
+// channel_at, and where S^T takes its blocks from the same tile (D = 128) the queries follow in the same order.
 __device__ __forceinline__ int chunk_place(int kc) { return 8 * ((kc >> 1) & 1) + 2 * (kc >> 2) + (kc & 1); }
 __device__ __forceinline__ int channel_at(int pos) {  // of a part's position
     const int pc = pos >> 3;
     return 8 * (4 * ((pc & 7) >> 1) + 2 * (pc >> 3) + (pc & 1)) + (pos & 7);
 }
 
-// This lane's 32 channels of one part of row 32 dw + rl + 8 I, as fp16 into its 128-byte-swizzled place. to0, to1: the
-// places of words 0 and 1 of row 32 dw + rl; words 2 and 3 lie a slice further on.
-template <int SF, int I, int SLICE>
-__device__ __forceinline__ void dequant(const uint4 &code, Scales sc, int rmax, int v, uint32_t to0, uint32_t to1) {
-    uint32_t s2[2];
+// The factors of a lane's 32 channels of one part of a row, as fp16 pairs: of words 0 and 1, and of 2 and 3.
+template <int SF>
+__device__ __forceinline__ void scale_halves(Scales sc, int rmax, int v, uint32_t (&s2)[2]) {
     if constexpr (SF == kScaleE8M0x32) {
         // 2^(X - rmax) from a float32 with that exponent (fp16 rounds what lies below 2^-25 to zero)
         const int e = max((int)((sc.x >> (8 * v)) & 0xFF) - rmax + 127, 0);
@@ -277,23 +282,58 @@ __device__ __forceinline__ void dequant(const uint4 &code, Scales sc, int rmax, 
             s2[h] = *reinterpret_cast<const uint32_t *>(&x2);
         }
     }
-    const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+}
+
+// Sixteen codes to eight fp16 pairs.
+__device__ __forceinline__ void scaled_halves(uint32_t w0, uint32_t w1, uint32_t s2, uint32_t (&o)[8]) {
+    uint32_t x[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t o[4];
-        e2m1_halves(w[k], o);
+    for (int k = 0; k < 2; ++k) {
+        e2m1_halves(k ? w1 : w0, x);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[b]), *reinterpret_cast<const __half2 *>(&s2[k >> 1]));
-            o[b] = *reinterpret_cast<const uint32_t *>(&h);
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&x[b]), *reinterpret_cast<const __half2 *>(&s2));
+            o[4 * k + b] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(((k & 1) ? to1 : to0) + I * 1024 + (k >> 1) * SLICE),
-                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                     : "memory");
     }
 }
 
+// Row 32 dw + rl + 8 I of a part into its place in the 128-byte-swizzled tile in shared memory. to0, to1: the places of
+// words 0 and 1 of row 32 dw + rl; words 2 and 3 lie a slice further on.
+template <int SF, int I, int SLICE>
+__device__ __forceinline__ void dequant_smem(const uint4 &code, Scales sc, int rmax, int v, uint32_t to0, uint32_t to1) {
+    uint32_t s2[2], o[8];
+    scale_halves<SF>(sc, rmax, v, s2);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        scaled_halves(k ? code.z : code.x, k ? code.w : code.y, s2[k], o);
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((z ? to1 : to0) + I * 1024 + k * SLICE), "r"(o[4 * z]),
+                         "r"(o[4 * z + 1]), "r"(o[4 * z + 2]), "r"(o[4 * z + 3])
+                         : "memory");
+    }
+}
+
+// Sixteen rows of half a part into tensor memory (32 columns of fp16 pairs): a is row lane / 4, b row lane / 4 + 8. Pair m
+// of lane v goes to column 8 (m / 2) + 2 v + m % 2 (the fragment of a 16x256b store), so channel 32 v + 2 m + e of
+// the part is the MMA's k = 16 (m / 2) + 4 v + 2 (m % 2) + e.
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&a)[8], const uint32_t (&b)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            taddr),
+        "r"(a[0]), "r"(a[1]), "r"(b[0]), "r"(b[1]), "r"(a[2]), "r"(a[3]), "r"(b[2]), "r"(b[3]), "r"(a[4]), "r"(a[5]),
+        "r"(b[4]), "r"(b[5]), "r"(a[6]), "r"(a[7]), "r"(b[6]), "r"(b[7])
+        : "memory");
+}
+
 // ---------------------------------------------------------------- main kernel
+// 17 warps leave 96 registers a thread. Saying so at the start of a role changes no split, but makes the compiler
+// allocate the role by itself: without it values that only rare paths need are spilled around the tile loop, and
+// with nearly all of L1 taken as shared memory every reload is a trip to L2 (2.2 ms against 1.64
+// at D = 512, 512 x 64 heads over 16384 blocks).
+__device__ __forceinline__ void keep_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
+
 // Two float32 at a time (one instruction for both), and 2^x to 2^-22 relative with results below 2^-126 as zero.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
@@ -394,6 +434,18 @@ __device__ __forceinline__ void reduce_columns(float2 (&v)[8]) {
     }
 }
 
+// ... with A (fp16 pairs) in tensor memory.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n"
+        :
+        : "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
 // B + 127 from what the dequantizing warps found (E8M0).
 __device__ __forceinline__ int base_of(const int (&b)[kTeamWarps]) {
     int m = b[0];
@@ -431,6 +483,7 @@ struct Cursor {
 // Shared state behind the operand buffers.
 struct Misc {
     uint64_t e_full[3][4], e_free[3][4], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free[2], r_full, drain;
+    uint64_t a_full[2], a_free[2], x_full[2];
     uint32_t tmem;
     int abort;
     alignas(16) float minus_rho[kCols], alpha[kCols], fac[kCols], jfac[kCols];
@@ -464,6 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             mbar_init(smem_u32(&ms->p_full[b]), kSoftmaxWarps);
             mbar_init(smem_u32(&ms->pv_done[b]), 1);
             mbar_init(smem_u32(&ms->o_free[b]), kSoftmaxWarps);
+            mbar_init(smem_u32(&ms->a_full[b]), kTeamWarps);
+            mbar_init(smem_u32(&ms->a_free[b]), 1);
+            mbar_init(smem_u32(&ms->x_full[b]), kTeamWarps);
         }
         mbar_init(smem_u32(&ms->q_full), kDequantWarps);
         mbar_init(smem_u32(&ms->r_full), kTeamWarps);
@@ -519,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         // nothing to do: fall through to the common end
     } else if (warp < kSoftmaxWarps) {
         // ================================================================ softmax and output
+        keep_registers();
         // S^T: 16 rows (blocks) a warp, and of them two a thread, in all 64 columns of which a thread has 16:
         // rows r0 and r0 + 8, columns 8 b + 2 (lane % 4) + {0, 1}, b = 0 .. 7 (the fragment that 16x256b loads
         // give and stmatrix takes). A column's factors are so read once for two rows.
@@ -534,22 +591,20 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         int n = 0;       // tiles done by this CTA
         Cursor c = start();
         while (c.left > 0) {
-            const Group gr = a.groups[c.g];
-            const int seg = c.seg, mp = seg & 1, lt0 = c.lt;
-            bool gave_up = false;
+            const int n_min = a.groups[c.g].n_min, mp = c.seg & 1;
+            const bool from_start = c.lt == 0;
+            bool gave_up = false, ok = true;
 #pragma unroll
             for (int b = 0; b < 8; ++b) lsum[b] = make_float2(0.f, 0.f);
             while (true) {
                 const bool first = c.first;
                 const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
-                bool ok = true;
-                if (n >= C::NP)  // P' is free: the O^T product of tile n - NP is done
-                    ok = wait(&ms->pv_done[(n - C::NP) & 1], ((n - C::NP) >> 1) & 1, abort);
-                ok = ok && wait(&ms->e_full[buf][0], use & 1, abort);
                 // the rows' exponents from B on: 0 for almost all of them
-                const float R0 = ms->rexp[buf][r0], R1 = ms->rexp[buf][r0 + 8];
+                const int xb = C::THROUGH_TMEM ? sb : buf;
+                ok = ok && (C::THROUGH_TMEM ? wait(&ms->x_full[sb], (n >> 1) & 1, abort) : wait(&ms->e_full[buf][0], use & 1, abort));
+                const float R0 = ms->rexp[xb][r0], R1 = ms->rexp[xb][r0 + 8];
                 const bool even = !__any_sync(0xffffffffu, R0 != 0.f || R1 != 0.f);
-                const bool masked = (c.lt + 1) * kTile > gr.n_min;
+                const bool masked = (c.lt + 1) * kTile > n_min;
                 ok = ok && wait(&ms->s_full[sb], (n >> 1) & 1, abort);
                 tc_fence_after();
                 float u[32];
@@ -649,13 +704,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 // P' = 2^(u - rho), fp16
                 const uint32_t Pn = p_addr + (n % C::NP) * C::P_BYTES;
 #pragma unroll
+                for (int k = 0; k < 32; ++k) u[k] = pow2(u[k]);
+                if (n >= C::NP)  // P' is free: the O^T product of tile n - NP is done (a failure shows in the next vote)
+                    ok = wait(&ms->pv_done[(n - C::NP) & 1], ((n - C::NP) >> 1) & 1, abort) && ok;
+#pragma unroll
                 for (int b = 0; b < 8; b += 2) {
                     uint32_t pk[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int k = 4 * b + 2 * q;
-                        u[k] = pow2(u[k]);
-                        u[k + 1] = pow2(u[k + 1]);
                         const __half2 hh = __floats2half2_rn(u[k], u[k + 1]);
                         pk[q] = *reinterpret_cast<const uint32_t *>(&hh);
                     }
@@ -680,20 +737,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                                        fma2(make_float2(u[4 * b + 2], u[4 * b + 3]), i1, lsum[b]));
                 }
                 ++n;
-                const bool last = c.mine == 1;
+                if (c.mine == 1) break;
                 step(c);
-                if (last) break;
             }
             if (gave_up) break;
             // ---------------- the group's output, or its partial
             reduce_columns<false>(lsum);
             *reinterpret_cast<float2 *>(&ms->wred[warp][2 * lane]) = lsum[0];
-            const bool ok = wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
+            ok = wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort) && ok;
             if (bar_or_n<kSoftmaxThreads>(!ok)) {
                 ms->abort = 1;
                 break;
             }
-            const bool whole = lt0 == 0 && (c.left > 0 ? c.lt == 0 : c.lt == gr.tiles);
+            const Group gr = a.groups[c.g];
+            const int seg = c.seg;
+            const bool whole = from_start && c.lt + 1 == gr.tiles;
             const int cols = gr.nq * a.H;
             const size_t row0 = (size_t)gr.q0 * a.H;
             // O^T holds E' = e 2^-(R - B) times P' over 2^B
@@ -718,56 +776,56 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             bar_sync_n<kSoftmaxThreads>();
             tc_fence_after();
 #pragma unroll 1
-            for (int dt = 0; dt < C::PARTS; ++dt) {
-                float o[32];
-                tmem_ld32(o_addr + kCols * dt, o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= unit;
-                if (dt == C::PARTS - 1) {  // O^T is read: the next group's products may start
+            for (int x = 0; x < 2 * C::PARTS; ++x) {  // 128 channels, 16 columns
+                float o[16];
+                const int col0 = 32 * hf + 16 * (x & 1), ch = 128 * (x >> 1) + channel_at(32 * (warp & 3) + lane);
+                tmem_ld16(o_addr + kCols * (x >> 1) + 16 * (x & 1), o);
+                if (x == 2 * C::PARTS - 1) {  // O^T is read: the next group's products may start
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[seg & 1]));
                 }
-                const int ch = 128 * dt + channel_at(32 * (warp & 3) + lane);
                 if (!whole) {
-                    float *dst = a.part_o + ((size_t)slot * kCols + 32 * hf) * D + ch;
+                    float *dst = a.part_o + ((size_t)slot * kCols + col0) * D + ch;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) dst[(size_t)k * D] = o[k];
+                    for (int k = 0; k < 16; ++k) dst[(size_t)k * D] = o[k] * unit;
                 } else {
-                    const float *jo = a.join_out + (row0 + 32 * hf) * D + ch;
+                    const float *jo = a.join_out + (row0 + col0) * D + ch;
+                    __nv_bfloat16 *dst = a.out + (row0 + col0 + (lane & 1)) * D + (ch & ~1);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
+                    for (int k = 0; k < 16; k += 2) {
                         float v[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int col = 32 * hf + k + e;
-                            v[e] = ms->fac[col] > 0.f || ms->fac[col] != ms->fac[col] ? o[k + e] * ms->fac[col] : 0.f;
-                            if (a.join_lse && col < cols && !(ms->jfac[col] == 0.f))
+                            const int col = col0 + k + e;
+                            const float f = ms->fac[col];
+                            v[e] = f == 0.f ? 0.f : o[k + e] * (f * unit);  // (a NaN goes on)
+                            if (a.join_lse && col < cols && ms->jfac[col] != 0.f)
                                 v[e] = fmaf(ms->jfac[col], jo[(size_t)(k + e) * D], v[e]);
                         }
                         // even lanes take column k, odd ones k + 1, with their neighbour's channel
                         const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[0] : v[1], 1);
-                        const int col = 32 * hf + k + (lane & 1);
-                        if (col < cols) {
-                            const __nv_bfloat162 h = (lane & 1) ? __floats2bfloat162_rn(got, v[1]) : __floats2bfloat162_rn(v[0], got);
-                            *reinterpret_cast<__nv_bfloat162 *>(a.out + (row0 + col) * D + (ch & ~1)) = h;
-                        }
+                        if (col0 + k + (lane & 1) < cols)
+                            *reinterpret_cast<__nv_bfloat162 *>(dst + (size_t)k * D) =
+                                (lane & 1) ? __floats2bfloat162_rn(got, v[1]) : __floats2bfloat162_rn(v[0], got);
                     }
                 }
             }
             if (tid < kCols) ms->minus_rho[tid] = 0.f;
             bar_sync_n<kSoftmaxThreads>();  // minus_rho, fac, wred belong to the next group from here on
+            step(c);
         }
     } else if (warp < kMmaWarp) {
         // ================================================================ dequantization, queries
-        // Two teams of four warps take the parts of the tile list in turn (D = 512: parts 0, 2 and 1, 3 of
-        // every tile; D = 128: every other tile).
+        keep_registers();
+        // Two teams of four warps. D = 512: the first brings every tile's parts into tensor memory for S^T, the second
+        // into shared memory for O^T, a tile later. D = 128: every other tile into shared memory, for both.
         const int dw = warp & 3, team = (warp - kSoftmaxWarps) >> 2, v = lane & 3, rl = lane >> 2;
         // this lane's rows of a tile are 32 dw + rl + 8 i, i = 0 .. 3
         const int j = 32 * dw + rl;
         const uint32_t place = smem_u32(E) + dw * 4096 + rl * 128;
         const uint32_t off0 = place + (((2 * v) ^ rl) << 4), off1 = place + (((2 * v + 1) ^ rl) << 4);
-        // the parts of a tile that this lane's registers hold: team, team + 2 (D = 512)
+        // parts ahead in registers
         constexpr int MINE = D == 512 ? 2 : 1;
         Cursor c = start();
         int slot_g = c.g, slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;  // the group of the rows asked for last
@@ -777,7 +835,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         // (the others are zero codes)
         struct Rows {
             const uint8_t *codes;
-            size_t row;
             int live;
         };
         auto rows_of = [&](const Cursor &x) {
@@ -788,8 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
             const int e = x.lt * kTile + j;
             Rows r;
-            r.row = (size_t)slot * a.cap + e;
-            r.codes = a.fp4 + r.row * (D / 2) + v * 16;
+            r.codes = a.fp4 + ((size_t)slot * a.cap + e) * (D / 2) + v * 16;
             r.live = n_max - e;
             return r;
         };
@@ -798,11 +854,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             for (int i = 0; i < 4; ++i)
                 to[i] = 8 * i < live ? load_here(src + i * 8 * (D / 2)) : make_uint4(0, 0, 0, 0);
         };
-        auto load_tile_scales = [&](Scales (&to)[4], const Rows &r) {
+        auto load_tile_scales = [&](Scales (&to)[4], const Rows &r) {  // of the group that rows_of went to last
+            constexpr int BYTES = 4 * (SF == kScaleE4M3x16 ? 2 : 1) * C::PARTS;  // of a row
+            const uint8_t *src = a.scale + ((size_t)slot * a.cap + (n_max - r.live)) * BYTES + (D == 512 ? BYTES / 4 * v : 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 to[i].x = to[i].y = 0;
-                if (8 * i < r.live) to[i] = load_scales<D, SF>(a, r.row + 8 * i, v);
+                if (8 * i < r.live) {
+                    to[i].x = load_word(src + 8 * i * BYTES);
+                    if constexpr (SF == kScaleE4M3x16) to[i].y = load_word(src + 8 * i * BYTES + 4);
+                }
             }
         };
         Rows rows = {};  // of the tile that code and sc hold
@@ -812,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             if (x.left > 0) {
                 rows = rows_of(x);
 #pragma unroll
-                for (int m = 0; m < MINE; ++m) load_codes(code[m], rows.codes + (D == 512 ? (team + 2 * m) * 64 : 0), rows.live);
+                for (int m = 0; m < MINE; ++m) load_codes(code[m], rows.codes + m * 64, rows.live);
                 load_tile_scales(sc, rows);
             }
         }
@@ -883,9 +944,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                                 const __half2 hh = __floats2half2_rn(f.x * inv, f.y * inv);
                                 o[z] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
-                            const int pc = (kc & ~15) + chunk_place(kc & 15);
-                            *reinterpret_cast<uint4 *>(Q + (pc >> 3) * C::QSLICE + (col >> 3) * 1024 + (col & 7) * 128 +
-                                                       (((pc & 7) ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if constexpr (C::THROUGH_TMEM) {
+                                // the k order of tmem_st_rows: two 8-byte pieces, k = 16 x + 4 w .. + 3
+                                const int w = (kc & 15) >> 2;
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    const int x = 2 * (kc & 3) + z;
+                                    *reinterpret_cast<uint2 *>(Q + (2 * (kc >> 4) + (x >> 2)) * C::QSLICE + (col >> 3) * 1024 +
+                                                               (col & 7) * 128 + (((2 * (x & 3) + (w >> 1)) ^ (col & 7)) << 4) +
+                                                               8 * (w & 1)) = make_uint2(o[2 * z], o[2 * z + 1]);
+                                }
+                            } else {
+                                const int pc = chunk_place(kc);
+                                *reinterpret_cast<uint4 *>(Q + (pc >> 3) * C::QSLICE + (col >> 3) * 1024 + (col & 7) * 128 +
+                                                           (((pc & 7) ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
                         }
                         if (sl == 0) {
                             ms->colmul[mp][col] = ldexpf(a.scale_log2, sq + base - 127);
@@ -897,32 +970,58 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
             }
-            Cursor nx = c;
-            step(nx);
             const int buf = n % C::NBUF, use = n / C::NBUF;
-            // one part into its place in shared memory, and the same part of this team's next tile on its way
-            auto part = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const Rows &next) {
+            auto words = [&](int i, int p) {
+                Scales x = sc[i];
+                if constexpr (D == 512) {  // part p's words are lane p's of the four
+                    x.x = __shfl_sync(0xffffffffu, x.x, (lane & ~3) | p);
+                    if constexpr (SF == kScaleE4M3x16) x.y = __shfl_sync(0xffffffffu, x.y, (lane & ~3) | p);
+                }
+                return x;
+            };
+            // one part into its place in shared memory, and the codes of the part at `then` on their way
+            auto to_smem = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const uint8_t *then, int live) {
                 if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort) && ok;
-                if (p == 0 && v == 0)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) ms->rexp[buf][j + 8 * i] = (float)(rmax[i] - base);
                 const uint32_t at = buf * C::E_BYTES + p * (2 * C::SLICE);
-                auto words = [&](int i) {
-                    Scales x = sc[i];
-                    if constexpr (D == 512) {  // part p's words are lane p's of the four
-                        x.x = __shfl_sync(0xffffffffu, x.x, (lane & ~3) | p);
-                        if constexpr (SF == kScaleE4M3x16) x.y = __shfl_sync(0xffffffffu, x.y, (lane & ~3) | p);
-                    }
-                    return x;
-                };
-                dequant<SF, 0, C::SLICE>(from[0], words(0), rmax[0], v, off0 + at, off1 + at);
-                dequant<SF, 1, C::SLICE>(from[1], words(1), rmax[1], v, off0 + at, off1 + at);
-                dequant<SF, 2, C::SLICE>(from[2], words(2), rmax[2], v, off0 + at, off1 + at);
-                dequant<SF, 3, C::SLICE>(from[3], words(3), rmax[3], v, off0 + at, off1 + at);
+                dequant_smem<SF, 0, C::SLICE>(from[0], words(0, p), rmax[0], v, off0 + at, off1 + at);
+                dequant_smem<SF, 1, C::SLICE>(from[1], words(1, p), rmax[1], v, off0 + at, off1 + at);
+                dequant_smem<SF, 2, C::SLICE>(from[2], words(2, p), rmax[2], v, off0 + at, off1 + at);
+                dequant_smem<SF, 3, C::SLICE>(from[3], words(3, p), rmax[3], v, off0 + at, off1 + at);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->e_full[buf][p]));
-                load_codes(from, next.codes + p * 64, next.live);
+                load_codes(from, then, live);
+            };
+            // ... into tensor memory
+            auto to_tmem = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const uint8_t *then, int live) {
+                // parts alternate between two buffers: this is use 2 n + p / 2 of its one
+                if (n >= 1 || p >= 2) ok = wait(&ms->a_free[p & 1], ((p >> 1) ^ 1) & 1, abort) && ok;
+                tc_fence_after();
+                const uint32_t at = tmem + C::TMEM_E + kCols * (p & 1) + ((uint32_t)(32 * dw) << 16);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t sx[2], sy[2], x[8], y[8];
+                    scale_halves<SF>(words(2 * h, p), rmax[2 * h], v, sx);
+                    scale_halves<SF>(words(2 * h + 1, p), rmax[2 * h + 1], v, sy);
+                    const uint32_t to = at + ((uint32_t)(16 * h) << 16);
+                    scaled_halves(from[2 * h].x, from[2 * h].y, sx[0], x);
+                    scaled_halves(from[2 * h + 1].x, from[2 * h + 1].y, sy[0], y);
+                    tmem_st_rows(to, x, y);
+                    scaled_halves(from[2 * h].z, from[2 * h].w, sx[1], x);
+                    scaled_halves(from[2 * h + 1].z, from[2 * h + 1].w, sy[1], y);
+                    tmem_st_rows(to + 32, x, y);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms->a_full[p & 1]));
+                load_codes(from, then, live);
+            };
+            auto post_exponents = [&](const int (&rmax)[4], int where) {
+                if (v == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ms->rexp[where][j + 8 * i] = (float)(rmax[i] - base);
+                }
             };
             auto exponents = [&](int (&rmax)[4]) {
 #pragma unroll
@@ -937,33 +1036,52 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             if constexpr (D == 512) {
                 int rmax[4];
                 exponents(rmax);
-                Rows next = {};
-                if (nx.left > 0) {
-                    next = rows_of(nx);
-                    load_tile_scales(nsc, next);
+                step(c);
+                if (team == 0) {
+                    if (n >= 2) ok = wait(&ms->s_free[n & 1], ((n >> 1) - 1) & 1, abort) && ok;  // rexp is read, too
+                    post_exponents(rmax, n & 1);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ms->x_full[n & 1]));
                 }
-#pragma unroll
-                for (int m = 0; m < MINE; ++m) part(code[m], team + 2 * m, rmax, next);
+#pragma unroll 1
+                for (int p = 0; p < C::PARTS; p += 2) {
+                    if (p == 2) {  // from here on the next tile's codes are loaded
+                        rows.live = 0;
+                        if (c.left > 0) rows = rows_of(c);
+                        load_tile_scales(nsc, rows);
+                    }
+                    const uint8_t *then = rows.codes + (p ^ 2) * 64;
+                    if (team == 0) {
+                        to_tmem(code[0], p, rmax, then, rows.live);
+                        to_tmem(code[1], p + 1, rmax, then + 64, rows.live);
+                    } else {
+                        to_smem(code[0], p, rmax, then, rows.live);
+                        to_smem(code[1], p + 1, rmax, then + 64, rows.live);
+                    }
+                }
                 if (!__all_sync(0xffffffffu, ok)) break;
-                rows = next;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
-            } else if ((n & 1) == team) {
-                Cursor n2 = nx;
-                if (nx.left > 0) step(n2);
-                int rmax[4];
-                exponents(rmax);
-                Rows next = {};
-                if (n2.left > 0) next = rows_of(n2);
-                load_tile_scales(nsc, next);
-                part(code[0], 0, rmax, next);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                rows = next;
+            } else {
+                if ((n & 1) == team) {
+                    int rmax[4];
+                    exponents(rmax);
+                    if (use >= 1) ok = wait(&ms->e_free[buf][0], (use - 1) & 1, abort) && ok;
+                    post_exponents(rmax, buf);
+                    Cursor x = c;
+                    step(x);
+                    if (x.left > 0) step(x);
+                    rows.live = 0;
+                    if (x.left > 0) rows = rows_of(x);
+                    load_tile_scales(nsc, rows);
+                    to_smem(code[0], 0, rmax, rows.codes, rows.live);
+                    if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
+                    for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
+                }
+                step(c);
             }
             ++n;
-            c = nx;
         }
         if (!ok) ms->abort = 1;
     } else if (elect_one()) {  // (the warp's other lanes wait at the common end)
@@ -985,13 +1103,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             if (n >= 2) ok = ok && wait(&ms->s_free[sb], ((n >> 1) - 1) & 1, abort);
 #pragma unroll 1
             for (int p = 0; p < C::PARTS; ++p) {
-                ok = ok && wait(&ms->e_full[buf][p], use & 1, abort);
+                // (use 2 n + p / 2 of a part's tensor memory)
+                ok = ok && (C::THROUGH_TMEM ? wait(&ms->a_full[p & 1], (p >> 1) & 1, abort) : wait(&ms->e_full[buf][p], use & 1, abort));
                 if (!ok) return;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)  // 16 channels each, 64 of a slice
-                    mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi,
-                        b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4), q_hi, IDESC_S, kk > 0 || p > 0);
+                for (int kk = 0; kk < 8; ++kk) {  // 16 channels each, 64 of a slice
+                    const uint32_t b_at = b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4);
+                    if constexpr (C::THROUGH_TMEM)
+                        mma_tmem(d, tmem + C::TMEM_E + kCols * (p & 1) + 8 * kk, b_at, q_hi, IDESC_S, kk > 0 || p > 0);
+                    else
+                        mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi, b_at, q_hi, IDESC_S, kk > 0 || p > 0);
+                }
+                if constexpr (C::THROUGH_TMEM) mma_commit(smem_u32(&ms->a_free[p & 1]));
                 a_lo += 2 * C::SLICE >> 4;
                 b_lo += 2 * C::QSLICE >> 4;
             }
@@ -1009,6 +1133,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             tc_fence_after();
 #pragma unroll 1
             for (int p = 0; p < C::PARTS; ++p) {
+                if constexpr (C::THROUGH_TMEM) {
+                    ok = ok && wait(&ms->e_full[0][p], n & 1, abort);
+                    if (!ok) return;
+                    tc_fence_after();
+                }
 #pragma unroll
                 for (int kj = 0; kj < kTile / 16; ++kj)  // 16 blocks each
                     mma(d, a_lo + (kj * 2048 >> 4), v_hi, b_lo + (kj * 2048 >> 4), p_hi, IDESC_O, kj > 0 || !first);
@@ -1020,17 +1149,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         };
         int n = 0, left = n_tiles, g = a.cta_g[blockIdx.x], seg = 0;
         int mine = min(left, (int)(a.groups[g].t0 + a.groups[g].tiles - t_begin));
-        bool before = false;  // the tile before was its group's first (several buffers: its O^T product is due)
+        bool before = false;  // the tile before was its group's first
         while (left > 0 && ok) {
             const int tiles = mine;
             for (int k = 0; k < tiles && ok; ++k, ++n) {
                 score(n, k == 0, k == tiles - 1, seg);
-                if constexpr (C::NBUF == 1) {
-                    value(n, k == 0, seg);
-                } else {  // S^T runs one tile ahead of O^T
-                    if (n > 0) value(n - 1, before, k == 0 ? seg - 1 : seg);
-                    before = k == 0;
-                }
+                if (n > 0) value(n - 1, before, k == 0 ? seg - 1 : seg);  // S^T runs one tile ahead of O^T
+                before = k == 0;
             }
             left -= tiles;
             if (left > 0) {
@@ -1039,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 mine = min(left, a.groups[g].tiles);
             }
         }
-        if (C::NBUF > 1 && ok) value(n - 1, before, seg);
+        if (ok) value(n - 1, before, seg);
         if (!ok) {
             ms->abort = 1;
             // nothing issued may still run when the CTA leaves
