@@ -163,41 +163,32 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-class _On:
-    """The device of a call's tensors made current, and the stream the call goes to made current on
-    it: `stream`, or that device's current one (what the call allocates then belongs to that stream)."""
+def _on(device, stream, call):
+    """call(raw stream) with the tensors' device current, on `stream` or that device's current one. What
+    the call allocates then belongs to that stream."""
+    import torch
 
-    def __init__(self, device, stream):
-        import torch
+    if device.type != "cuda":
+        raise CsaError(f"tensors must be on a CUDA device, not {device}")
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(_raw_stream(device.index))
+    with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+        return call(torch.cuda.current_stream().cuda_stream)
 
-        self.guard, self.stream = None, stream
-        if device.type != "cuda":
-            raise CsaError(f"tensors must be on a CUDA device, not {device}")
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        elif device.index is not None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
 
-    def __enter__(self):
-        import torch
+def _raw_stream(index):
+    """The handle of a device's current stream (without a stream object where PyTorch offers that: 3 us less)."""
+    import torch
 
-        if self.guard is not None:
-            self.guard.__enter__()
-        stream = torch.cuda.current_stream() if self.stream is None else self.stream
-        return ctypes.c_void_p(stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _expect(what, name, t, device, dtype, shape):
-    """One tensor of a call: on `device`, of `dtype`, dense, with this shape (None: any extent)."""
-    if t.device != device or t.dtype != dtype or not t.is_contiguous() or len(t.shape) != len(shape) or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)):
-        want = ", ".join("*" if n is None else str(n) for n in shape)
-        raise CsaError(f"{what}: {name} must be a dense {dtype} tensor [{want}] on {device}, not "
-                       f"{t.dtype} {list(t.shape)} on {t.device}")
+    """One tensor of a call: on `device`, of `dtype`, dense, of this shape."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise CsaError(f"{what}: {name} must be a dense {dtype} tensor {list(shape)} on {device}, not "
+                       f"{t.dtype} {list(t.shape)}{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
 
 
 @dataclass
@@ -453,9 +444,11 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
     import torch
 
     lib, what = load_library(), "hca_shared_attend"
-    device, bf16, f32, i32 = q.device, torch.bfloat16, torch.float32, torch.int32
-    _expect(what, "q", q, device, bf16, (None, None, cache.dim))
+    device, f32, i32 = q.device, torch.float32, torch.int32
+    if q.dim() != 3:
+        raise CsaError(f"{what}: q must be [queries, heads, dim], not {list(q.shape)}")
     n, heads, D = q.shape
+    _expect(what, "q", q, device, torch.bfloat16, (n, heads, cache.dim))
     if cache.fp4.device != device:
         raise CsaError(f"{what}: cache is on {cache.fp4.device}, q on {device}")
     _expect(what, "q_offsets", q_offsets, device, i32, (cache.batch + 1,))
@@ -466,21 +459,22 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
     if join_lse is not None:
         _expect(what, "join_lse", join_lse, device, f32, (n, heads))
     if out is not None:
-        _expect(what, "out", out, device, bf16, (n, heads, D))
+        _expect(what, "out", out, device, torch.bfloat16, (n, heads, D))
     if lse is not None:
         _expect(what, "lse", lse, device, f32, (n, heads))
-    c = cache.c_struct()
-    with _On(device, stream) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            need = lib.hca_shared_attend_workspace(ctypes.byref(c), n, heads)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        _check(lib.hca_shared_attend(ctypes.byref(c), q.data_ptr(), n, heads, q_offsets.data_ptr(), _ptr(q_pos),
-                                     _ptr(join_out), _ptr(join_lse), D ** -0.5 if softmax_scale is None else
-                                     softmax_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                                     workspace.nbytes, s), what)
-    return out
+    c = ctypes.byref(cache.c_struct())
+
+    def call(s):
+        to = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib.hca_shared_attend_workspace(c, n, heads) or 256, dtype=torch.uint8, device=device)
+        _check(lib.hca_shared_attend(c, q.data_ptr(), n, heads, q_offsets.data_ptr(), _ptr(q_pos), _ptr(join_out),
+                                     _ptr(join_lse), D ** -0.5 if softmax_scale is None else softmax_scale,
+                                     to.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, s), what)
+        return to
+
+    return _on(device, stream, call)
 
 
 def csa_cache_copy_workspace(dst: Cache, n_jobs: int, keep_cols: int = 0) -> int:
@@ -496,38 +490,43 @@ def csa_cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, keep=None, max_bl
     import torch
 
     lib, what = load_library(), "csa_cache_copy"
-    device, n = src.fp4.device, src_slot.shape[0]
+    device, n, i32 = src.fp4.device, src_slot.shape[0] if src_slot.dim() else -1, torch.int32
     if dst.fp4.device != device:
         raise CsaError(f"{what}: src is on {device}, dst on {dst.fp4.device}")
-    _expect(what, "src_slot", src_slot, device, torch.int32, (None,))
-    _expect(what, "dst_slot", dst_slot, device, torch.int32, (n,))
+    _expect(what, "src_slot", src_slot, device, i32, (n,))
+    _expect(what, "dst_slot", dst_slot, device, i32, (n,))
     cols = 0
     if keep is not None:
-        _expect(what, "keep", keep, device, torch.int32, (n, None))
-        cols = keep.shape[1]
+        cols = keep.shape[-1] if keep.dim() else 0
+        _expect(what, "keep", keep, device, i32, (n, cols))
         if cols == 0:
             raise CsaError(f"{what}: keep needs a column (-1 in it keeps nothing)")
     if max_blocks is not None:
-        _expect(what, "max_blocks", max_blocks, device, torch.int32, (n,))
+        _expect(what, "max_blocks", max_blocks, device, i32, (n,))
     cs = src.c_struct()
     cd = cs if dst is src else dst.c_struct()
-    with _On(device, stream) as s:
-        if workspace is None:
-            need = lib.csa_cache_copy_workspace(ctypes.byref(cd), n, cols)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+    def call(s):
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib.csa_cache_copy_workspace(ctypes.byref(cd), n, cols) or 256, dtype=torch.uint8,
+                             device=device)
         _check(lib.csa_cache_copy(ctypes.byref(cs), ctypes.byref(cd), n, src_slot.data_ptr(), dst_slot.data_ptr(),
-                                  _ptr(keep), cols, _ptr(max_blocks), workspace.data_ptr(), workspace.nbytes, s), what)
+                                  _ptr(keep), cols, _ptr(max_blocks), ws.data_ptr(), ws.nbytes, s), what)
+
+    _on(device, stream, call)
 
 
 def _vectors(what, name, t):
     import torch
 
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    kind = CSA_BF16 if t.dtype is torch.bfloat16 else CSA_F32
+    if kind == CSA_F32 and t.dtype is not torch.float32:
         raise CsaError(f"{what}: {name} must be bfloat16 or float32, not {t.dtype}")
-    if t.dim() not in (2, 3) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    step = t.stride()
+    if len(step) not in (2, 3) or (step[-1] != 1 and t.shape[-1] > 1):
         raise CsaError(f"{what}: {name} must be [rows, (heads,) dim] with adjacent channels")
-    return _CVectors(t.data_ptr(), CSA_BF16 if t.dtype == torch.bfloat16 else CSA_F32, t.stride(0),
-                     t.stride(1) if t.dim() == 3 else 0)
+    return _CVectors(t.data_ptr(), kind, step[0], step[1] if len(step) == 3 else 0)
 
 
 def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layout: int = CSA_ROPE_PAIRS,
@@ -545,17 +544,19 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
     if out is not None and (out.shape != x.shape or out.device != x.device or
                             (out_dtype is not None and out.dtype != out_dtype)):
         raise CsaError(f"{what}: out must match x's shape and device, and out_dtype")
+    rot = 2 * inv_freq.shape[0] if inv_freq.dim() else 0
     _expect(what, "pos", pos, x.device, torch.int32, (rows,))
-    _expect(what, "inv_freq", inv_freq, x.device, torch.float32, (None,))
-    rot = 2 * inv_freq.shape[0]
+    _expect(what, "inv_freq", inv_freq, x.device, torch.float32, (rot // 2,))
     rope = _CRope(inv_freq.data_ptr(), dim - rot if rot_begin is None else rot_begin, rot, layout, mscale)
-    with _On(x.device, stream) as s:
-        if out is None:
-            out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        co = _vectors(what, "out", out)
-        _check(lib.csa_rotary(ctypes.byref(cx), ctypes.byref(co), rows, heads, dim, ctypes.byref(rope),
-                              pos.data_ptr(), int(inverse), s), what)
-    return out
+
+    def call(s):
+        to = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+        co = cx if to is x else _vectors(what, "out", to)
+        _check(lib.csa_rotary(ctypes.byref(cx), ctypes.byref(co), rows, heads, dim, ctypes.byref(rope), pos.data_ptr(),
+                              int(inverse), s), what)
+        return to
+
+    return _on(x.device, stream, call)
 
 
 def csa_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = CSA_ROPE_SCALE_NONE,

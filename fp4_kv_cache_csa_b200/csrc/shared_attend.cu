@@ -67,6 +67,10 @@ constexpr int kExponentSpan = 40, kEvenBelow = 10, kEvenAbove = 12;
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
+// Calls of up to so many groups and slots are planned by every CTA of the main kernel for itself: a launch, and the
+// wait for its 5 us, less.
+constexpr int kFusedGroups = 256;
+constexpr int kMostCtas = 256;
 
 template <int D>
 struct Cfg {
@@ -83,7 +87,7 @@ struct Cfg {
     static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T, then two parts of E'
     static constexpr int TMEM_E = TMEM_O + PARTS * kCols;
     static constexpr int TMEM_COLS = TMEM_E + (THROUGH_TMEM ? 2 * kCols : 0) <= 256 ? 256 : 512;
-    static constexpr int MISC = 6144;
+    static constexpr int MISC = 16384;
     static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
 };
 
@@ -107,7 +111,7 @@ struct SharedArgs {
     int *gbase;                // [batch + 1] first group of each slot
     long long *cta_t;          // [G + 1] first tile of each CTA's range
     int *cta_g;                // [G] first group
-    int *n_groups;
+    int *merge_g;              // [G] the group that a CTA's first tile lies inside of and that it is the first to, or -1
     float *part_o, *part_rho, *part_l;
     int batch, cap, m, Nq, H, per_group, G, groups_max;
     float scale_log2;
@@ -120,6 +124,116 @@ __device__ __forceinline__ int visible_of(const SharedArgs &a, int b, int i) {
 __device__ __forceinline__ int query_bound(const SharedArgs &a, int b) { return min(max(a.q_offsets[b], 0), a.Nq); }
 
 // ---------------------------------------------------------------- schedule
+// Where CTA c's share of all units begins: the nearest tile boundary, and the group of the first tile from there on.
+struct Share {
+    long long t;
+    int first;
+};
+template <typename T>
+__device__ __forceinline__ Share share_of(const T *gunits, const Group *groups, int NG, T tiles, T units, int c, int G) {
+    Share s = {(long long)tiles, max(NG - 1, 0)};
+    if (c < G && NG > 0) {
+        const T ub = (T)((long long)units * c / G);
+        int lo = 0, hi = NG - 1;  // last group with gunits[g] <= ub
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (gunits[mid] <= ub) lo = mid; else hi = mid - 1;
+        }
+        const int n = groups[lo].tiles;
+        const T x = ub - gunits[lo] - (T)kStartUnits;
+        const int k = x > 0 ? (int)min((x + (T)kTileUnits / 2) / (T)kTileUnits, (T)n) : 0;
+        s.t = groups[lo].t0 + k;
+        s.first = k == n && lo + 1 < NG ? lo + 1 : lo;
+    }
+    return s;
+}
+// The group that has tiles before and behind CTA c's first one, if no CTA before c begins inside it, too; else -1.
+template <typename T>
+__device__ __forceinline__ int merge_of(const Group *groups, const T *cta_t, const int *cta_g, int c) {
+    if (c == 0) return -1;
+    const int g = cta_g[c];
+    const long long t = cta_t[c], t0 = groups[g].t0;
+    return t > t0 && t < t0 + groups[g].tiles && cta_t[c - 1] <= t0 ? g : -1;
+}
+
+// The record of group g of slot b (its first group gb): queries, visible blocks, tiles.
+__device__ __forceinline__ Group group_of(const SharedArgs &a, int b, int first) {
+    Group r = {};
+    r.b = b;
+    r.q0 = query_bound(a, b) + first * a.per_group;
+    r.nq = min(a.per_group, query_bound(a, b + 1) - r.q0);
+    r.n_min = 0x7fffffff;
+    for (int k = 0; k < r.nq; ++k) {
+        const int n = visible_of(a, b, r.q0 + k);
+        r.n_max = max(r.n_max, n);
+        r.n_min = min(r.n_min, n);
+    }
+    r.tiles = max(1, (r.n_max + kTile - 1) / kTile);
+    return r;
+}
+__device__ __forceinline__ int groups_in(const SharedArgs &a, int b) {
+    return (max(query_bound(a, b + 1) - query_bound(a, b), 0) + a.per_group - 1) / a.per_group;
+}
+
+// The plan of a call of at most kFusedGroups groups and slots, by all threads of a CTA that want their own share: the
+// groups into tab, the shares of CTAs c and c + 1 into first / t. scratch: 4 KB of shared memory. CTA 0 also
+// writes what shared_merge_kernel reads.
+__device__ __noinline__ void plan_small(const SharedArgs &a, int *scratch, Group *tab, int (&first)[2], int (&t)[2]) {
+    __shared__ int tmp[32];
+    int *gbase = scratch, *gunits = scratch + kFusedGroups + 1, *cta_t = gunits + kFusedGroups + 1, *cta_g = cta_t + kMostCtas + 1;
+    const int tid = threadIdx.x;
+    const int mine = tid < a.batch ? groups_in(a, tid) : 0;
+    const int before = block_inclusive_scan<int>(mine, tmp);
+    if (tid < a.batch) gbase[tid + 1] = min(before, kFusedGroups);
+    if (tid == 0) gbase[0] = 0;
+    __syncthreads();
+    const int NG = min(gbase[a.batch], a.groups_max);  // (groups_max only cuts offsets that are not ascending)
+    Group r = {};
+    if (tid < NG) {
+        int lo = 0, hi = a.batch - 1;  // the slot with gbase[b] <= g < gbase[b + 1]
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (gbase[mid + 1] <= tid) lo = mid + 1; else hi = mid;
+        }
+        r = group_of(a, lo, tid - gbase[lo]);
+    }
+    const int units = tid < NG ? (int)(kStartUnits + kTileUnits * r.tiles) : 0;
+    const int tin = block_inclusive_scan<int>(r.tiles, tmp), uin = block_inclusive_scan<int>(units, tmp);
+    if (tid < NG) {
+        r.t0 = tin - r.tiles;
+        tab[tid] = r;
+        gunits[tid + 1] = uin;
+    }
+    if (tid == 0) gunits[0] = 0;
+    if (tid == blockDim.x - 1) {
+        tmp[0] = tin;
+        tmp[1] = uin;
+    }
+    __syncthreads();
+    const int tiles_all = tmp[0], units_all = tmp[1];
+    const int c = blockIdx.x;
+    if (tid < 2 || (c == 0 && tid <= a.G)) {
+        const int which = c + tid;
+        const Share x = share_of<int>(gunits, tab, NG, tiles_all, units_all, which, a.G);
+        if (tid < 2) {
+            t[tid] = (int)x.t;
+            first[tid] = x.first;
+        }
+        if (c == 0) {
+            cta_t[which] = (int)x.t;
+            if (which < a.G) cta_g[which] = x.first;
+        }
+    }
+    __syncthreads();
+    if (c == 0) {
+        for (int k = tid; k <= a.G; k += blockDim.x) {
+            a.cta_t[k] = cta_t[k];
+            if (k < a.G) a.merge_g[k] = NG > 0 ? merge_of(tab, cta_t, cta_g, k) : -1;
+        }
+        if (tid < NG) a.groups[tid] = r;
+    }
+}
+
 // One thread block: groups of every slot, their tiles, and the CTAs' ranges. A group
 // without a visible block keeps one (wholly masked) tile, so that its output is written
 // like any other.
@@ -130,8 +244,7 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
     long long carry = 0;
     for (int base = 0; base < a.batch; base += blockDim.x) {
         const int b = base + threadIdx.x;
-        long long g = 0;
-        if (b < a.batch) g = (max(query_bound(a, b + 1) - query_bound(a, b), 0) + a.per_group - 1) / a.per_group;
+        const long long g = b < a.batch ? groups_in(a, b) : 0;
         const long long incl = block_inclusive_scan<long long>(g, tmp);
         if (b < a.batch) a.gbase[b + 1] = (int)min(carry + incl, (long long)a.groups_max);
         if (threadIdx.x == blockDim.x - 1) round_total = incl;
@@ -155,23 +268,13 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
                 const int mid = (lo + hi) >> 1;
                 if (a.gbase[mid + 1] <= g) lo = mid + 1; else hi = mid;
             }
-            r.b = lo;
-            r.q0 = query_bound(a, lo) + (g - a.gbase[lo]) * a.per_group;
-            r.nq = min(a.per_group, query_bound(a, lo + 1) - r.q0);
-            r.n_max = 0;
-            r.n_min = 0x7fffffff;
-            for (int k = 0; k < r.nq; ++k) {
-                const int n = visible_of(a, lo, r.q0 + k);
-                r.n_max = max(r.n_max, n);
-                r.n_min = min(r.n_min, n);
-            }
-            tiles = max(1, (r.n_max + kTile - 1) / kTile);
+            r = group_of(a, lo, g - a.gbase[lo]);
+            tiles = r.tiles;
             units = kStartUnits + kTileUnits * tiles;
         }
         const long long tin = block_inclusive_scan<long long>(tiles, tmp);
         if (g < NG) {
             r.t0 = tcarry + tin - tiles;
-            r.tiles = tiles;
             a.groups[g] = r;
         }
         if (threadIdx.x == blockDim.x - 1) round_total = tin;
@@ -185,32 +288,18 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
         ucarry += round_total;
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        a.gunits[0] = 0;
-        *a.n_groups = NG;
-    }
+    if (threadIdx.x == 0) a.gunits[0] = 0;
     __threadfence_block();
     __syncthreads();
     // CTA c begins at the tile boundary nearest to its share of the units
     for (int c = threadIdx.x; c <= a.G; c += blockDim.x) {
-        long long t = tcarry;
-        int first = max(NG - 1, 0);
-        if (c < a.G && NG > 0) {
-            const long long ub = ucarry * c / a.G;
-            int lo = 0, hi = NG - 1;  // last group with gunits[g] <= ub
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.gunits[mid] <= ub) lo = mid; else hi = mid - 1;
-            }
-            const Group r = a.groups[lo];
-            const long long x = ub - a.gunits[lo] - kStartUnits;
-            const long long k = x > 0 ? min((x + kTileUnits / 2) / kTileUnits, (long long)r.tiles) : 0;
-            t = r.t0 + k;
-            first = k == r.tiles && lo + 1 < NG ? lo + 1 : lo;
-        }
-        a.cta_t[c] = t;
-        if (c < a.G) a.cta_g[c] = first;
+        const Share x = share_of(a.gunits, a.groups, NG, tcarry, ucarry, c, a.G);
+        a.cta_t[c] = x.t;
+        if (c < a.G) a.cta_g[c] = x.first;
     }
+    __threadfence_block();
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.G; c += blockDim.x) a.merge_g[c] = merge_of(a.groups, a.cta_t, a.cta_g, c);
 }
 
 // ---------------------------------------------------------------- operands
@@ -490,12 +579,15 @@ struct Misc {
     float wred[kSoftmaxWarps][kCols];
     float colmul[2][kCols];  // scale_log2 * 2^(sQ + B) of each column, by segment parity
     int nvis[2][kCols];
+    Group tab[kFusedGroups];  // the groups, where the kernel planned itself
+    int plan_first[2], plan_t[2];
+    int begin_g, begin_lt, n_tiles;  // the CTA's range: its first group and tile of it, and its tiles
     float rexp[3][kTile];    // R_j - B
     int base[2][4];          // largest exponent byte of each dequantizing warp's rows, by segment parity
 };
-static_assert(sizeof(Misc) <= 6144, "Misc exceeds its space");
+static_assert(sizeof(Misc) <= 16384, "Misc exceeds its space");
 
-template <int D, int SF>
+template <int D, int SF, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid_constant__ SharedArgs a) {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -542,17 +634,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     const volatile int *abort = &ms->abort;
     grid_dep_wait();
     grid_dep_launch();
-    const long long t_begin = a.cta_t[blockIdx.x];
-    const int n_tiles = (int)(a.cta_t[blockIdx.x + 1] - t_begin);
-
+    if constexpr (FUSED) {
+        plan_small(a, reinterpret_cast<int *>(smem), ms->tab, ms->plan_first, ms->plan_t);
+    }
+    if (tid == 0) {
+        const long long t = FUSED ? ms->plan_t[0] : a.cta_t[blockIdx.x];
+        ms->begin_g = FUSED ? ms->plan_first[0] : a.cta_g[blockIdx.x];
+        ms->n_tiles = (int)((FUSED ? ms->plan_t[1] : a.cta_t[blockIdx.x + 1]) - t);
+        ms->begin_lt = (int)(t - (FUSED ? ms->tab : a.groups)[ms->begin_g].t0);
+    }
+    __syncthreads();
+    auto group = [&](int g) -> const Group & { return FUSED ? ms->tab[g] : a.groups[g]; };
     auto start = [&]() {
         Cursor c;
-        c.g = a.cta_g[blockIdx.x];
+        c.g = ms->begin_g;
         c.seg = 0;
-        const Group g = a.groups[c.g];
-        c.lt = (int)(t_begin - g.t0);
-        c.left = n_tiles;
-        c.mine = min(n_tiles, g.tiles - c.lt);
+        c.lt = ms->begin_lt;
+        c.left = ms->n_tiles;
+        c.mine = min(c.left, group(c.g).tiles - c.lt);
         c.first = true;
         return c;
     };
@@ -566,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             ++c.g;
             ++c.seg;
             c.lt = 0;
-            c.mine = min(c.left, a.groups[c.g].tiles);
+            c.mine = min(c.left, group(c.g).tiles);
             c.first = true;
         }
     };
 
-    if (n_tiles <= 0) {
+    if (ms->n_tiles <= 0) {
         // nothing to do: fall through to the common end
     } else if (warp < kSoftmaxWarps) {
         // ================================================================ softmax and output
@@ -591,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         int n = 0;       // tiles done by this CTA
         Cursor c = start();
         while (c.left > 0) {
-            const int n_min = a.groups[c.g].n_min, mp = c.seg & 1;
+            const int n_min = group(c.g).n_min, mp = c.seg & 1;
             const bool from_start = c.lt == 0;
             bool gave_up = false, ok = true;
 #pragma unroll
@@ -749,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 ms->abort = 1;
                 break;
             }
-            const Group gr = a.groups[c.g];
+            const Group gr = group(c.g);
             const int seg = c.seg;
             const bool whole = from_start && c.lt + 1 == gr.tiles;
             const int cols = gr.nq * a.H;
@@ -828,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         // parts ahead in registers
         constexpr int MINE = D == 512 ? 2 : 1;
         Cursor c = start();
-        int slot_g = c.g, slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;  // the group of the rows asked for last
+        int slot_g = c.g, slot = group(c.g).b, n_max = group(c.g).n_max;  // the group of the rows asked for last
         uint4 code[MINE][4];
         Scales sc[4], nsc[4];
         // this lane's first row of a tile (its codes of part 0), and how many rows from there on are visible
@@ -840,8 +939,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         auto rows_of = [&](const Cursor &x) {
             if (x.g != slot_g) {
                 slot_g = x.g;
-                slot = a.groups[slot_g].b;
-                n_max = a.groups[slot_g].n_max;
+                slot = group(slot_g).b;
+                n_max = group(slot_g).n_max;
             }
             const int e = x.lt * kTile + j;
             Rows r;
@@ -881,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         bool ok = true;
         while (c.left > 0) {
             if (c.first) {
-                const Group gr = a.groups[c.g];
+                const Group gr = group(c.g);
                 // the queries of the group: column = row q0 * H + column of q; per column 2^-sQ
                 if (c.seg >= 1) ok = wait(&ms->q_free, (c.seg - 1) & 1, abort);
                 if (c.seg >= 2) ok = ok && wait(&ms->o_free[c.seg & 1], ((c.seg - 2) >> 1) & 1, abort);
@@ -1147,8 +1246,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
             mma_commit(smem_u32(&ms->pv_done[n & 1]));
         };
-        int n = 0, left = n_tiles, g = a.cta_g[blockIdx.x], seg = 0;
-        int mine = min(left, (int)(a.groups[g].t0 + a.groups[g].tiles - t_begin));
+        int n = 0, left = ms->n_tiles, g = ms->begin_g, seg = 0;
+        int mine = min(left, group(g).tiles - ms->begin_lt);
         bool before = false;  // the tile before was its group's first
         while (left > 0 && ok) {
             const int tiles = mine;
@@ -1161,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             if (left > 0) {
                 ++g;
                 ++seg;
-                mine = min(left, a.groups[g].tiles);
+                mine = min(left, group(g).tiles);
             }
         }
         if (ok) value(n - 1, before, seg);
@@ -1184,7 +1283,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
 // ---------------------------------------------------------------- merge
 // A group that several CTAs worked on: blockIdx.x + 1 is a CTA whose range begins inside the group, the
 // first such CTA merges it. blockIdx.y: 8 columns, blockIdx.z: 128 channels.
-constexpr int kMergeCols = 8, kMostParts = 256;
+constexpr int kMergeCols = 8, kMostParts = kMostCtas;
 
 __global__ void __launch_bounds__(256) shared_merge_kernel(SharedArgs a, int D) {
     __shared__ int slots[kMostParts];
@@ -1192,18 +1291,10 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(SharedArgs a, int D) 
     __shared__ float s_join[kMergeCols];
     __shared__ int np_s;
     grid_dep_wait();
-    const int c = blockIdx.x + 1, NG = *a.n_groups;
-    const long long tb = a.cta_t[c];
-    if (NG == 0) return;
-    int lo = 0, hi = NG - 1;  // the group that holds tile tb - 1
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.groups[mid].t0 + a.groups[mid].tiles < tb) lo = mid + 1; else hi = mid;
-    }
-    const Group gr = a.groups[lo];
+    const int c = blockIdx.x + 1, g = a.merge_g[c];
+    if (g < 0) return;
+    const Group gr = a.groups[g];
     const long long t1 = gr.t0 + gr.tiles;
-    if (tb <= gr.t0 || tb >= t1) return;              // the boundary lies between two groups
-    if (c > 1 && a.cta_t[c - 1] > gr.t0) return;         // an earlier CTA begins inside the group, too
     const int cols = gr.nq * a.H, c0 = blockIdx.y * kMergeCols;
     if (c0 >= cols) return;
     const int nc = min(kMergeCols, cols - c0);
@@ -1291,7 +1382,7 @@ int most_groups(int batch, int Nq, int per_group) {
 }
 
 struct Layout {
-    size_t groups, gunits, gbase, cta_t, cta_g, n_groups, part_o, part_rho, part_l, bytes;
+    size_t groups, gunits, gbase, cta_t, cta_g, merge_g, part_o, part_rho, part_l, bytes;
 };
 
 Layout layout_of(int batch, int Nq, int H, int D, int G) {
@@ -1308,7 +1399,7 @@ Layout layout_of(int batch, int Nq, int H, int D, int G) {
     l.gbase = take(4 * ((size_t)batch + 1));
     l.cta_t = take(8 * ((size_t)G + 1));
     l.cta_g = take(4 * (size_t)G);
-    l.n_groups = take(4);
+    l.merge_g = take(4 * (size_t)G);
     l.part_o = take(4 * (size_t)2 * G * kCols * D);
     l.part_rho = take(4 * (size_t)2 * G * kCols);
     l.part_l = take(4 * (size_t)2 * G * kCols);
@@ -1316,12 +1407,23 @@ Layout layout_of(int batch, int Nq, int H, int D, int G) {
     return l;
 }
 
-template <int D, int SF>
+template <int D, int SF, bool FUSED>
 cudaError_t launch_main(const SharedArgs &a, cudaStream_t s) {
-    cudaError_t err = cudaFuncSetAttribute(shared_attend_kernel<D, SF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Cfg<D>::SMEM);
+    const cudaError_t err = cudaFuncSetAttribute(shared_attend_kernel<D, SF, FUSED>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
     if (err != cudaSuccess) return err;
-    return launch_pdl(shared_attend_kernel<D, SF>, dim3(a.G), dim3(kThreads), (size_t)Cfg<D>::SMEM, s, a);
+    if (!FUSED) return launch_pdl(shared_attend_kernel<D, SF, FUSED>, dim3(a.G), dim3(kThreads), (size_t)Cfg<D>::SMEM, s, a);
+    // the call's first kernel: nothing before it on the stream may still be running
+    shared_attend_kernel<D, SF, FUSED><<<a.G, kThreads, Cfg<D>::SMEM, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D, int SF>
+cudaError_t launch_planned(const SharedArgs &a, cudaStream_t s) {
+    if (a.batch <= kFusedGroups && a.groups_max <= kFusedGroups) return launch_main<D, SF, true>(a, s);
+    shared_schedule_kernel<<<1, 1024, 0, s>>>(a);
+    const cudaError_t err = cudaGetLastError();
+    return err != cudaSuccess ? err : launch_main<D, SF, false>(a, s);
 }
 
 }  // namespace
@@ -1355,7 +1457,7 @@ cudaError_t launch_shared_attend(const csa_cache &c, const void *q, int Nq, int 
     a.gbase = reinterpret_cast<int *>(base + l.gbase);
     a.cta_t = reinterpret_cast<long long *>(base + l.cta_t);
     a.cta_g = reinterpret_cast<int *>(base + l.cta_g);
-    a.n_groups = reinterpret_cast<int *>(base + l.n_groups);
+    a.merge_g = reinterpret_cast<int *>(base + l.merge_g);
     a.part_o = reinterpret_cast<float *>(base + l.part_o);
     a.part_rho = reinterpret_cast<float *>(base + l.part_rho);
     a.part_l = reinterpret_cast<float *>(base + l.part_l);
@@ -1368,12 +1470,10 @@ cudaError_t launch_shared_attend(const csa_cache &c, const void *q, int Nq, int 
     a.G = G;
     a.groups_max = most_groups(c.batch, Nq, a.per_group);
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
-    shared_schedule_kernel<<<1, 1024, 0, s>>>(a);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
+    cudaError_t err;
     const bool e4m3 = c.scale_fmt == CSA_SCALE_E4M3_16;
-    if (D == 512) err = e4m3 ? launch_main<512, kScaleE4M3x16>(a, s) : launch_main<512, kScaleE8M0x32>(a, s);
-    else err = e4m3 ? launch_main<128, kScaleE4M3x16>(a, s) : launch_main<128, kScaleE8M0x32>(a, s);
+    if (D == 512) err = e4m3 ? launch_planned<512, kScaleE4M3x16>(a, s) : launch_planned<512, kScaleE8M0x32>(a, s);
+    else err = e4m3 ? launch_planned<128, kScaleE4M3x16>(a, s) : launch_planned<128, kScaleE8M0x32>(a, s);
     if (err != cudaSuccess) return err;
     if (G < 2) return cudaSuccess;
     return launch_pdl(shared_merge_kernel, dim3(G - 1, kCols / kMergeCols, D / 128), dim3(256), 0, s, a, D);
