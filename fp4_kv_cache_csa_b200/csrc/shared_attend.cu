@@ -63,13 +63,14 @@ constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 // (groups down to 2^-13 of the row's largest, which a row at B has down to 2^-23), and then takes none: R = 0. Others
 // take theirs, but at least B - 40: what that flushes to zero lies below 2^-64 of the first tile's scale,
 // and no sum leaves float32's range over all-zero rows (scale byte 0).
+constexpr int kNoRow = 1024;  // of a row behind the last visible one: its factors come out 0
 constexpr int kExponentSpan = 40, kEvenBelow = 10, kEvenAbove = 12;
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
-// Calls of up to so many groups and slots are planned by every CTA of the main kernel for itself: a launch, and the
-// wait for its 5 us, less.
-constexpr int kFusedGroups = 256;
+// Calls of up to so many groups and slots are planned in shared memory (2.5 instead of 5.6 us; planned by every CTA of
+// the main kernel for itself, a launch less, they made that kernel's registers spill: 94 -> 106 us at 32 queries).
+constexpr int kSmallGroups = 512;
 constexpr int kMostCtas = 256;
 
 template <int D>
@@ -87,7 +88,7 @@ struct Cfg {
     static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T, then two parts of E'
     static constexpr int TMEM_E = TMEM_O + PARTS * kCols;
     static constexpr int TMEM_COLS = TMEM_E + (THROUGH_TMEM ? 2 * kCols : 0) <= 256 ? 256 : 512;
-    static constexpr int MISC = 16384;
+    static constexpr int MISC = 6144;
     static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
 };
 
@@ -175,16 +176,15 @@ __device__ __forceinline__ int groups_in(const SharedArgs &a, int b) {
     return (max(query_bound(a, b + 1) - query_bound(a, b), 0) + a.per_group - 1) / a.per_group;
 }
 
-// The plan of a call of at most kFusedGroups groups and slots, by all threads of a CTA that want their own share: the
-// groups into tab, the shares of CTAs c and c + 1 into first / t. scratch: 4 KB of shared memory. CTA 0 also
-// writes what shared_merge_kernel reads.
-__device__ __noinline__ void plan_small(const SharedArgs &a, int *scratch, Group *tab, int (&first)[2], int (&t)[2]) {
-    __shared__ int tmp[32];
-    int *gbase = scratch, *gunits = scratch + kFusedGroups + 1, *cta_t = gunits + kFusedGroups + 1, *cta_g = cta_t + kMostCtas + 1;
+// The plan of a call of at most kSmallGroups groups and slots: the same steps, on shared memory.
+__global__ void __launch_bounds__(kSmallGroups) shared_plan_kernel(SharedArgs a) {
+    __shared__ int tmp[32], gbase[kSmallGroups + 1], gunits[kSmallGroups + 1], cta_t[kMostCtas + 1], cta_g[kMostCtas];
+    __shared__ Group tab[kSmallGroups];
     const int tid = threadIdx.x;
+    grid_dep_launch();
     const int mine = tid < a.batch ? groups_in(a, tid) : 0;
     const int before = block_inclusive_scan<int>(mine, tmp);
-    if (tid < a.batch) gbase[tid + 1] = min(before, kFusedGroups);
+    if (tid < a.batch) gbase[tid + 1] = min(before, kSmallGroups);
     if (tid == 0) gbase[0] = 0;
     __syncthreads();
     const int NG = min(gbase[a.batch], a.groups_max);  // (groups_max only cuts offsets that are not ascending)
@@ -202,6 +202,7 @@ __device__ __noinline__ void plan_small(const SharedArgs &a, int *scratch, Group
     if (tid < NG) {
         r.t0 = tin - r.tiles;
         tab[tid] = r;
+        a.groups[tid] = r;
         gunits[tid + 1] = uin;
     }
     if (tid == 0) gunits[0] = 0;
@@ -211,32 +212,18 @@ __device__ __noinline__ void plan_small(const SharedArgs &a, int *scratch, Group
     }
     __syncthreads();
     const int tiles_all = tmp[0], units_all = tmp[1];
-    const int c = blockIdx.x;
-    if (tid < 2 || (c == 0 && tid <= a.G)) {
-        const int which = c + tid;
-        const Share x = share_of<int>(gunits, tab, NG, tiles_all, units_all, which, a.G);
-        if (tid < 2) {
-            t[tid] = (int)x.t;
-            first[tid] = x.first;
-        }
-        if (c == 0) {
-            cta_t[which] = (int)x.t;
-            if (which < a.G) cta_g[which] = x.first;
-        }
+    for (int c = tid; c <= a.G; c += blockDim.x) {
+        const Share x = share_of<int>(gunits, tab, NG, tiles_all, units_all, c, a.G);
+        cta_t[c] = (int)x.t;
+        a.cta_t[c] = x.t;
+        if (c < a.G) a.cta_g[c] = cta_g[c] = x.first;
     }
     __syncthreads();
-    if (c == 0) {
-        for (int k = tid; k <= a.G; k += blockDim.x) {
-            a.cta_t[k] = cta_t[k];
-            if (k < a.G) a.merge_g[k] = NG > 0 ? merge_of(tab, cta_t, cta_g, k) : -1;
-        }
-        if (tid < NG) a.groups[tid] = r;
-    }
+    for (int c = tid; c < a.G; c += blockDim.x) a.merge_g[c] = NG > 0 ? merge_of(tab, cta_t, cta_g, c) : -1;
 }
 
-// One thread block: groups of every slot, their tiles, and the CTAs' ranges. A group
-// without a visible block keeps one (wholly masked) tile, so that its output is written
-// like any other.
+// ... and of any call. One thread block: groups of every slot, their tiles, and the CTAs' ranges. A group without a
+// visible block keeps one (wholly masked) tile, so that its output is written like any other.
 __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
     __shared__ long long tmp[32];
     __shared__ long long round_total;
@@ -579,15 +566,12 @@ struct Misc {
     float wred[kSoftmaxWarps][kCols];
     float colmul[2][kCols];  // scale_log2 * 2^(sQ + B) of each column, by segment parity
     int nvis[2][kCols];
-    Group tab[kFusedGroups];  // the groups, where the kernel planned itself
-    int plan_first[2], plan_t[2];
-    int begin_g, begin_lt, n_tiles;  // the CTA's range: its first group and tile of it, and its tiles
     float rexp[3][kTile];    // R_j - B
     int base[2][4];          // largest exponent byte of each dequantizing warp's rows, by segment parity
 };
-static_assert(sizeof(Misc) <= 16384, "Misc exceeds its space");
+static_assert(sizeof(Misc) <= 6144, "Misc exceeds its space");
 
-template <int D, int SF, bool FUSED>
+template <int D, int SF>
 __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid_constant__ SharedArgs a) {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -634,24 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     const volatile int *abort = &ms->abort;
     grid_dep_wait();
     grid_dep_launch();
-    if constexpr (FUSED) {
-        plan_small(a, reinterpret_cast<int *>(smem), ms->tab, ms->plan_first, ms->plan_t);
-    }
-    if (tid == 0) {
-        const long long t = FUSED ? ms->plan_t[0] : a.cta_t[blockIdx.x];
-        ms->begin_g = FUSED ? ms->plan_first[0] : a.cta_g[blockIdx.x];
-        ms->n_tiles = (int)((FUSED ? ms->plan_t[1] : a.cta_t[blockIdx.x + 1]) - t);
-        ms->begin_lt = (int)(t - (FUSED ? ms->tab : a.groups)[ms->begin_g].t0);
-    }
-    __syncthreads();
-    auto group = [&](int g) -> const Group & { return FUSED ? ms->tab[g] : a.groups[g]; };
+    const long long t_begin = a.cta_t[blockIdx.x];
+    const int n_tiles = (int)(a.cta_t[blockIdx.x + 1] - t_begin);
     auto start = [&]() {
         Cursor c;
-        c.g = ms->begin_g;
+        c.g = a.cta_g[blockIdx.x];
         c.seg = 0;
-        c.lt = ms->begin_lt;
-        c.left = ms->n_tiles;
-        c.mine = min(c.left, group(c.g).tiles - c.lt);
+        c.lt = (int)(t_begin - a.groups[c.g].t0);
+        c.left = n_tiles;
+        c.mine = min(c.left, a.groups[c.g].tiles - c.lt);
         c.first = true;
         return c;
     };
@@ -665,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             ++c.g;
             ++c.seg;
             c.lt = 0;
-            c.mine = min(c.left, group(c.g).tiles);
+            c.mine = min(c.left, a.groups[c.g].tiles);
             c.first = true;
         }
     };
 
-    if (ms->n_tiles <= 0) {
+    if (n_tiles <= 0) {
         // nothing to do: fall through to the common end
     } else if (warp < kSoftmaxWarps) {
         // ================================================================ softmax and output
@@ -690,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         int n = 0;       // tiles done by this CTA
         Cursor c = start();
         while (c.left > 0) {
-            const int n_min = group(c.g).n_min, mp = c.seg & 1;
+            const int n_min = a.groups[c.g].n_min, mp = c.seg & 1;
             const bool from_start = c.lt == 0;
             bool gave_up = false, ok = true;
 #pragma unroll
@@ -848,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 ms->abort = 1;
                 break;
             }
-            const Group gr = group(c.g);
+            const Group gr = a.groups[c.g];
             const int seg = c.seg;
             const bool whole = from_start && c.lt + 1 == gr.tiles;
             const int cols = gr.nq * a.H;
@@ -927,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         // parts ahead in registers
         constexpr int MINE = D == 512 ? 2 : 1;
         Cursor c = start();
-        int slot_g = c.g, slot = group(c.g).b, n_max = group(c.g).n_max;  // the group of the rows asked for last
+        int slot_g = c.g, slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;  // the group of the rows asked for last
         uint4 code[MINE][4];
         Scales sc[4], nsc[4];
         // this lane's first row of a tile (its codes of part 0), and how many rows from there on are visible
@@ -939,8 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         auto rows_of = [&](const Cursor &x) {
             if (x.g != slot_g) {
                 slot_g = x.g;
-                slot = group(slot_g).b;
-                n_max = group(slot_g).n_max;
+                slot = a.groups[slot_g].b;
+                n_max = a.groups[slot_g].n_max;
             }
             const int e = x.lt * kTile + j;
             Rows r;
@@ -948,10 +923,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             r.live = n_max - e;
             return r;
         };
+        // (rows behind the last visible one load that one again; their factors are 0)
         auto load_codes = [&](uint4 (&to)[4], const uint8_t *src, int live) {
+            if (live >= 32 - rl) {  // the warp's 32 rows are all visible
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to[i] = 8 * i < live ? load_here(src + i * 8 * (D / 2)) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) to[i] = load_here(src + i * 8 * (D / 2));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[i] = load_here(src + (min(8 * i, live - 1) * (D / 2)));
+            }
         };
         auto load_tile_scales = [&](Scales (&to)[4], const Rows &r) {  // of the group that rows_of went to last
             constexpr int BYTES = 4 * (SF == kScaleE4M3x16 ? 2 : 1) * C::PARTS;  // of a row
@@ -966,13 +946,20 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
         };
         Rows rows = {};  // of the tile that code and sc hold
+#pragma unroll
+        for (int m = 0; m < MINE; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) code[m][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i].x = sc[i].y = nsc[i].x = nsc[i].y = 0;
         {
             Cursor x = c;
             if (D == 128 && team == 1) step(x);
             if (x.left > 0) {
                 rows = rows_of(x);
 #pragma unroll
-                for (int m = 0; m < MINE; ++m) load_codes(code[m], rows.codes + m * 64, rows.live);
+                for (int m = 0; m < MINE; ++m)
+                    if (n_max > 0) load_codes(code[m], rows.codes + m * 64, rows.live);
                 load_tile_scales(sc, rows);
             }
         }
@@ -980,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         bool ok = true;
         while (c.left > 0) {
             if (c.first) {
-                const Group gr = group(c.g);
+                const Group gr = a.groups[c.g];
                 // the queries of the group: column = row q0 * H + column of q; per column 2^-sQ
                 if (c.seg >= 1) ok = wait(&ms->q_free, (c.seg - 1) & 1, abort);
                 if (c.seg >= 2) ok = ok && wait(&ms->o_free[c.seg & 1], ((c.seg - 2) >> 1) & 1, abort);
@@ -1089,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->e_full[buf][p]));
-                load_codes(from, then, live);
+                if (then) load_codes(from, then, live);
             };
             // ... into tensor memory
             auto to_tmem = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const uint8_t *then, int live) {
@@ -1114,12 +1101,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->a_full[p & 1]));
-                load_codes(from, then, live);
+                if (then) load_codes(from, then, live);
             };
             auto post_exponents = [&](const int (&rmax)[4], int where) {
                 if (v == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ms->rexp[where][j + 8 * i] = (float)(rmax[i] - base);
+                    for (int i = 0; i < 4; ++i) ms->rexp[where][j + 8 * i] = rmax[i] == kNoRow ? 0.f : (float)(rmax[i] - base);
                 }
             };
             auto exponents = [&](int (&rmax)[4]) {
@@ -1128,7 +1115,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     rmax[i] = base;
                     if constexpr (SF == kScaleE8M0x32) {
                         const int m = row_exponent(sc[i].x), d = m - base;
-                        if (8 * i < rows.live && (d < -kEvenBelow || d > kEvenAbove)) rmax[i] = max(m, base - kExponentSpan);
+                        if (d < -kEvenBelow || d > kEvenAbove) rmax[i] = max(m, base - kExponentSpan);
+                        if (8 * i >= rows.live) rmax[i] = kNoRow;
                     }
                 }
             };
@@ -1145,17 +1133,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
 #pragma unroll 1
                 for (int p = 0; p < C::PARTS; p += 2) {
                     if (p == 2) {  // from here on the next tile's codes are loaded
-                        rows.live = 0;
+                        rows = {};
                         if (c.left > 0) rows = rows_of(c);
                         load_tile_scales(nsc, rows);
                     }
-                    const uint8_t *then = rows.codes + (p ^ 2) * 64;
+                    // (no codes to load behind the last tile, and of a group without visible blocks)
+                    const uint8_t *then = rows.codes && n_max > 0 ? rows.codes + (p ^ 2) * 64 : nullptr;
+                    const uint8_t *then1 = then ? then + 64 : nullptr;
                     if (team == 0) {
                         to_tmem(code[0], p, rmax, then, rows.live);
-                        to_tmem(code[1], p + 1, rmax, then + 64, rows.live);
+                        to_tmem(code[1], p + 1, rmax, then1, rows.live);
                     } else {
                         to_smem(code[0], p, rmax, then, rows.live);
-                        to_smem(code[1], p + 1, rmax, then + 64, rows.live);
+                        to_smem(code[1], p + 1, rmax, then1, rows.live);
                     }
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -1170,10 +1160,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     Cursor x = c;
                     step(x);
                     if (x.left > 0) step(x);
-                    rows.live = 0;
+                    rows = {};
                     if (x.left > 0) rows = rows_of(x);
                     load_tile_scales(nsc, rows);
-                    to_smem(code[0], 0, rmax, rows.codes, rows.live);
+                    to_smem(code[0], 0, rmax, n_max > 0 ? rows.codes : nullptr, rows.live);
                     if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
@@ -1246,8 +1236,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             }
             mma_commit(smem_u32(&ms->pv_done[n & 1]));
         };
-        int n = 0, left = ms->n_tiles, g = ms->begin_g, seg = 0;
-        int mine = min(left, group(g).tiles - ms->begin_lt);
+        int n = 0, left = n_tiles, g = a.cta_g[blockIdx.x], seg = 0;
+        int mine = min(left, (int)(a.groups[g].t0 + a.groups[g].tiles - t_begin));
         bool before = false;  // the tile before was its group's first
         while (left > 0 && ok) {
             const int tiles = mine;
@@ -1260,7 +1250,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             if (left > 0) {
                 ++g;
                 ++seg;
-                mine = min(left, group(g).tiles);
+                mine = min(left, a.groups[g].tiles);
             }
         }
         if (ok) value(n - 1, before, seg);
@@ -1407,23 +1397,12 @@ Layout layout_of(int batch, int Nq, int H, int D, int G) {
     return l;
 }
 
-template <int D, int SF, bool FUSED>
-cudaError_t launch_main(const SharedArgs &a, cudaStream_t s) {
-    const cudaError_t err = cudaFuncSetAttribute(shared_attend_kernel<D, SF, FUSED>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
-    if (err != cudaSuccess) return err;
-    if (!FUSED) return launch_pdl(shared_attend_kernel<D, SF, FUSED>, dim3(a.G), dim3(kThreads), (size_t)Cfg<D>::SMEM, s, a);
-    // the call's first kernel: nothing before it on the stream may still be running
-    shared_attend_kernel<D, SF, FUSED><<<a.G, kThreads, Cfg<D>::SMEM, s>>>(a);
-    return cudaGetLastError();
-}
-
 template <int D, int SF>
-cudaError_t launch_planned(const SharedArgs &a, cudaStream_t s) {
-    if (a.batch <= kFusedGroups && a.groups_max <= kFusedGroups) return launch_main<D, SF, true>(a, s);
-    shared_schedule_kernel<<<1, 1024, 0, s>>>(a);
-    const cudaError_t err = cudaGetLastError();
-    return err != cudaSuccess ? err : launch_main<D, SF, false>(a, s);
+cudaError_t launch_main(const SharedArgs &a, cudaStream_t s) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(shared_attend_kernel<D, SF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(shared_attend_kernel<D, SF>, dim3(a.G), dim3(kThreads), (size_t)Cfg<D>::SMEM, s, a);
 }
 
 }  // namespace
@@ -1470,10 +1449,13 @@ cudaError_t launch_shared_attend(const csa_cache &c, const void *q, int Nq, int 
     a.G = G;
     a.groups_max = most_groups(c.batch, Nq, a.per_group);
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
-    cudaError_t err;
+    if (a.batch <= kSmallGroups && a.groups_max <= kSmallGroups) shared_plan_kernel<<<1, kSmallGroups, 0, s>>>(a);
+    else shared_schedule_kernel<<<1, 1024, 0, s>>>(a);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
     const bool e4m3 = c.scale_fmt == CSA_SCALE_E4M3_16;
-    if (D == 512) err = e4m3 ? launch_planned<512, kScaleE4M3x16>(a, s) : launch_planned<512, kScaleE8M0x32>(a, s);
-    else err = e4m3 ? launch_planned<128, kScaleE4M3x16>(a, s) : launch_planned<128, kScaleE8M0x32>(a, s);
+    if (D == 512) err = e4m3 ? launch_main<512, kScaleE4M3x16>(a, s) : launch_main<512, kScaleE8M0x32>(a, s);
+    else err = e4m3 ? launch_main<128, kScaleE4M3x16>(a, s) : launch_main<128, kScaleE8M0x32>(a, s);
     if (err != cudaSuccess) return err;
     if (G < 2) return cudaSuccess;
     return launch_pdl(shared_merge_kernel, dim3(G - 1, kCols / kMergeCols, D / 128), dim3(256), 0, s, a, D);
