@@ -454,6 +454,19 @@ __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity, const
     return done || mbar_wait_ab<false>(smem_u32(bar), parity, abort);
 }
 
+// Whether a barrier's phase is complete, without waiting.
+__device__ __forceinline__ bool is_done(const uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // One lane of the warp, the same one every time (the compiler then knows that a single thread runs).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -1182,78 +1195,86 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         const uint64_t dv = desc_sw128(smem_u32(E), C::SLICE, 1024), dp = desc_sw128(smem_u32(P), 8192, 1024);
         const uint32_t e_hi = (uint32_t)(de >> 32), q_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32),
                        p_hi = (uint32_t)(dp >> 32);
+        // Parts of S^T (up to two tiles ahead) and of O^T are issued as their operands become ready, whichever
+        // is: waiting for one of the two in turn held the other up.
+        struct Role {
+            int n, p;           // tile, part of it
+            int g, seg, mine;   // its group, the group's number within the CTA, tiles left of it
+            bool first;         // first tile of the group within the CTA
+        };
+        const int g0 = a.cta_g[blockIdx.x];
+        Role s = {0, 0, g0, 0, min(n_tiles, (int)(a.groups[g0].t0 + a.groups[g0].tiles - t_begin)), true};
+        Role v = s;
+        auto next_tile = [&](Role &r) {
+            r.p = 0;
+            ++r.n;
+            r.first = false;
+            if (--r.mine == 0 && r.n < n_tiles) {
+                ++r.g;
+                ++r.seg;
+                r.mine = min(n_tiles - r.n, a.groups[r.g].tiles);
+                r.first = true;
+            }
+        };
         bool ok = true;
-        // S^T of tile n
-        auto score = [&](int n, bool first, bool last, int seg) {
-            const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
-            uint32_t a_lo = (uint32_t)de + buf * (C::E_BYTES >> 4), b_lo = (uint32_t)dq;
-            const uint32_t d = tmem + kCols * sb;
-            if (first) ok = ok && wait(&ms->q_full, seg & 1, abort);
-            if (n >= 2) ok = ok && wait(&ms->s_free[sb], ((n >> 1) - 1) & 1, abort);
-#pragma unroll 1
-            for (int p = 0; p < C::PARTS; ++p) {
-                // (use 2 n + p / 2 of a part's tensor memory)
-                ok = ok && (C::THROUGH_TMEM ? wait(&ms->a_full[p & 1], (p >> 1) & 1, abort) : wait(&ms->e_full[buf][p], use & 1, abort));
-                if (!ok) return;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {  // 16 channels each, 64 of a slice
-                    const uint32_t b_at = b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4);
-                    if constexpr (C::THROUGH_TMEM)
-                        mma_tmem(d, tmem + C::TMEM_E + kCols * (p & 1) + 8 * kk, b_at, q_hi, IDESC_S, kk > 0 || p > 0);
-                    else
-                        mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi, b_at, q_hi, IDESC_S, kk > 0 || p > 0);
-                }
-                if constexpr (C::THROUGH_TMEM) mma_commit(smem_u32(&ms->a_free[p & 1]));
-                a_lo += 2 * C::SLICE >> 4;
-                b_lo += 2 * C::QSLICE >> 4;
-            }
-            mma_commit(smem_u32(&ms->s_full[sb]));
-            if (last) mma_commit(smem_u32(&ms->q_free));
-        };
-        // O^T += of tile n
-        auto value = [&](int n, bool first, int seg) {
-            const int buf = n % C::NBUF;
-            uint32_t a_lo = (uint32_t)dv + buf * (C::E_BYTES >> 4), d = tmem + C::TMEM_O;
-            const uint32_t b_lo = (uint32_t)dp + (n % C::NP) * (C::P_BYTES >> 4);
-            ok = ok && wait(&ms->p_full[n % C::NP], (n / C::NP) & 1, abort);
-            if (first && seg >= 1) ok = ok && wait(&ms->o_free[(seg - 1) & 1], ((seg - 1) >> 1) & 1, abort);
-            if (!ok) return;
-            tc_fence_after();
-#pragma unroll 1
-            for (int p = 0; p < C::PARTS; ++p) {
-                if constexpr (C::THROUGH_TMEM) {
-                    ok = ok && wait(&ms->e_full[0][p], n & 1, abort);
-                    if (!ok) return;
+        long long since = clock64();
+        while (v.n < n_tiles) {
+            bool moved = false;
+            if (v.n < s.n) {  // O^T += of tile v.n
+                const int buf = v.n % C::NBUF;
+                bool ready = v.p > 0 || (is_done(&ms->p_full[v.n % C::NP], (v.n / C::NP) & 1) &&
+                                         (!v.first || v.seg == 0 || is_done(&ms->o_free[(v.seg - 1) & 1], ((v.seg - 1) >> 1) & 1)));
+                if (C::THROUGH_TMEM && ready) ready = is_done(&ms->e_full[0][v.p], v.n & 1);
+                if (ready) {
                     tc_fence_after();
-                }
+                    const uint32_t a_lo = (uint32_t)dv + ((buf * C::E_BYTES + v.p * 2 * C::SLICE) >> 4);
+                    const uint32_t b_lo = (uint32_t)dp + (v.n % C::NP) * (C::P_BYTES >> 4), d = tmem + C::TMEM_O + kCols * v.p;
 #pragma unroll
-                for (int kj = 0; kj < kTile / 16; ++kj)  // 16 blocks each
-                    mma(d, a_lo + (kj * 2048 >> 4), v_hi, b_lo + (kj * 2048 >> 4), p_hi, IDESC_O, kj > 0 || !first);
-                mma_commit(smem_u32(&ms->e_free[buf][p]));
-                a_lo += 2 * C::SLICE >> 4;
-                d += kCols;
+                    for (int kj = 0; kj < kTile / 16; ++kj)  // 16 blocks each
+                        mma(d, a_lo + (kj * 2048 >> 4), v_hi, b_lo + (kj * 2048 >> 4), p_hi, IDESC_O, kj > 0 || !v.first);
+                    mma_commit(smem_u32(&ms->e_free[buf][v.p]));
+                    if (++v.p == C::PARTS) {
+                        mma_commit(smem_u32(&ms->pv_done[v.n & 1]));
+                        next_tile(v);
+                    }
+                    moved = true;
+                }
             }
-            mma_commit(smem_u32(&ms->pv_done[n & 1]));
-        };
-        int n = 0, left = n_tiles, g = a.cta_g[blockIdx.x], seg = 0;
-        int mine = min(left, (int)(a.groups[g].t0 + a.groups[g].tiles - t_begin));
-        bool before = false;  // the tile before was its group's first
-        while (left > 0 && ok) {
-            const int tiles = mine;
-            for (int k = 0; k < tiles && ok; ++k, ++n) {
-                score(n, k == 0, k == tiles - 1, seg);
-                if (n > 0) value(n - 1, before, k == 0 ? seg - 1 : seg);  // S^T runs one tile ahead of O^T
-                before = k == 0;
+            if (s.n < n_tiles) {  // S^T of tile s.n
+                const int buf = s.n % C::NBUF, sb = s.n & 1;
+                bool ready = s.p > 0 || ((!s.first || is_done(&ms->q_full, s.seg & 1)) &&
+                                         (s.n < 2 || is_done(&ms->s_free[sb], ((s.n >> 1) - 1) & 1)));
+                // (use 2 n + p / 2 of a part's tensor memory)
+                if (ready) ready = C::THROUGH_TMEM ? is_done(&ms->a_full[s.p & 1], (s.p >> 1) & 1)
+                                                   : is_done(&ms->e_full[buf][s.p], (s.n / C::NBUF) & 1);
+                if (ready) {
+                    tc_fence_after();
+                    const uint32_t a_lo = (uint32_t)de + ((buf * C::E_BYTES + s.p * 2 * C::SLICE) >> 4);
+                    const uint32_t b_lo = (uint32_t)dq + (s.p * 2 * C::QSLICE >> 4), d = tmem + kCols * sb;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {  // 16 channels each, 64 of a slice
+                        const uint32_t b_at = b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4);
+                        if constexpr (C::THROUGH_TMEM)
+                            mma_tmem(d, tmem + C::TMEM_E + kCols * (s.p & 1) + 8 * kk, b_at, q_hi, IDESC_S, kk > 0 || s.p > 0);
+                        else
+                            mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi, b_at, q_hi, IDESC_S, kk > 0 || s.p > 0);
+                    }
+                    if constexpr (C::THROUGH_TMEM) mma_commit(smem_u32(&ms->a_free[s.p & 1]));
+                    if (++s.p == C::PARTS) {
+                        mma_commit(smem_u32(&ms->s_full[sb]));
+                        if (s.mine == 1) mma_commit(smem_u32(&ms->q_free));
+                        next_tile(s);
+                    }
+                    moved = true;
+                }
             }
-            left -= tiles;
-            if (left > 0) {
-                ++g;
-                ++seg;
-                mine = min(left, a.groups[g].tiles);
+            if (moved) {
+                since = clock64();
+            } else if (*abort || clock64() - since > kWaitCycles) {
+                ok = false;
+                break;
             }
         }
-        if (ok) value(n - 1, before, seg);
         if (!ok) {
             ms->abort = 1;
             // nothing issued may still run when the CTA leaves
