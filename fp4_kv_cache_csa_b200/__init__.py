@@ -228,7 +228,8 @@ class Cache:
         return self.idx_key.shape[2] * (2 if self.idx_dtype == CSA_IDX_MXFP4 else 1)
 
     def c_struct(self) -> _CCache:
-        return _CCache(self.batch, self.dim, self.block, self.capacity, _ptr(self.fp4), _ptr(self.scale),
+        batch, capacity, half = self.fp4.shape
+        return _CCache(batch, 2 * half, self.block, capacity, self.fp4.data_ptr(), _ptr(self.scale),
                        _ptr(self.idx_key), self.idx_dim, self.idx_dtype, _ptr(self.n_blocks), _ptr(self.status),
                        self.scale_fmt, _ptr(self.idx_key_scale))
 
