@@ -552,7 +552,7 @@ __device__ __forceinline__ void finish(float rho, float l, bool join, float othe
     jf = 0.f;
     if (join) {
         const float top = fmaxf(lse, other);
-        if (top != -INFINITY) {
+        if (top != -INFINITY || other != other) {
             const float x = expf(lse - top), y = expf(other - top);
             f *= x / (x + y);
             jf = y / (x + y);

@@ -276,6 +276,24 @@ def test_nan_behind_the_visible_blocks():
     run(c, [0, 5, 9], 16)
 
 
+@pytest.mark.parametrize("H", [16, 64])
+def test_a_nan_of_the_other_part_stays_one(H):
+    import torch
+
+    import fp4_kv_cache_csa_b200 as csa
+
+    # slot 0 has no blocks, slot 1 some, slot 2 so many that several thread blocks share the group
+    c = random_cache(3, 20000, 512, n=[0, 300, 20000])
+    q = dev(datagen.normal_bf16((6, H, 512), 4, 1))
+    offs = dev(np.array([0, 2, 4, 6], np.int32))
+    jo, jl = torch.ones(6, H, 512, device="cuda"), torch.zeros(6, H, device="cuda")
+    jl[::2, 3] = math.nan
+    lse = torch.empty(6, H, device="cuda")
+    out = csa.hca_shared_attend(c, q, offs, join_out=jo, join_lse=jl, lse=lse)
+    assert torch.equal(lse.isnan(), jl.isnan())
+    assert torch.equal(out.isnan(), jl.isnan()[..., None].expand(out.shape))
+
+
 def test_offsets_beyond_32_bits():
     import torch
 
