@@ -170,6 +170,8 @@ def _on(device, stream, call):
 
     if device.type != "cuda":
         raise CsaError(f"tensors must be on a CUDA device, not {device}")
+    if stream is not None and stream.device != device:
+        raise CsaError(f"stream is of {stream.device}, tensors are on {device}")
     if stream is None and device.index == torch.cuda.current_device():
         return call(_raw_stream(device.index))
     with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
@@ -189,6 +191,12 @@ def _expect(what, name, t, device, dtype, shape):
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise CsaError(f"{what}: {name} must be a dense {dtype} tensor {list(shape)} on {device}, not "
                        f"{t.dtype} {list(t.shape)}{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
+
+
+def _expect_workspace(what, ws, device):
+    """A caller's workspace: dense, and on `device` (the library checks its size)."""
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise CsaError(f"{what}: workspace must be a dense tensor on {device}, not on {ws.device}")
 
 
 @dataclass
@@ -463,13 +471,12 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
         _expect(what, "out", out, device, torch.bfloat16, (n, heads, D))
     if lse is not None:
         _expect(what, "lse", lse, device, f32, (n, heads))
+    _expect_workspace(what, workspace, device)
     c = ctypes.byref(cache.c_struct())
 
     def call(s):
         to = torch.empty_like(q) if out is None else out
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib.hca_shared_attend_workspace(c, n, heads) or 256, dtype=torch.uint8, device=device)
+        ws = _workspace(lib.hca_shared_attend_workspace(c, n, heads), workspace, device)
         _check(lib.hca_shared_attend(c, q.data_ptr(), n, heads, q_offsets.data_ptr(), _ptr(q_pos), _ptr(join_out),
                                      _ptr(join_lse), D ** -0.5 if softmax_scale is None else softmax_scale,
                                      to.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, s), what)
@@ -504,14 +511,12 @@ def csa_cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, keep=None, max_bl
             raise CsaError(f"{what}: keep needs a column (-1 in it keeps nothing)")
     if max_blocks is not None:
         _expect(what, "max_blocks", max_blocks, device, i32, (n,))
+    _expect_workspace(what, workspace, device)
     cs = src.c_struct()
     cd = cs if dst is src else dst.c_struct()
 
     def call(s):
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib.csa_cache_copy_workspace(ctypes.byref(cd), n, cols) or 256, dtype=torch.uint8,
-                             device=device)
+        ws = _workspace(lib.csa_cache_copy_workspace(ctypes.byref(cd), n, cols), workspace, device)
         _check(lib.csa_cache_copy(ctypes.byref(cs), ctypes.byref(cd), n, src_slot.data_ptr(), dst_slot.data_ptr(),
                                   _ptr(keep), cols, _ptr(max_blocks), ws.data_ptr(), ws.nbytes, s), what)
 

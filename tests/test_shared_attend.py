@@ -77,3 +77,15 @@ def test_binding_refusals(lib):
             csa.hca_shared_attend(**dict(dict(cache=c, q=q, q_offsets=offs), **kw))
     with pytest.raises(csa.CsaError, match="CUDA device"):
         csa.hca_shared_attend(c, q, offs)
+
+
+def test_other_streams_and_workspaces_are_refused():
+    class Stream:
+        device = torch.device("cuda:1")
+
+    with pytest.raises(csa.CsaError, match="stream is of cuda:1"):
+        csa._on(torch.device("cuda:0"), Stream(), lambda s: None)
+    with pytest.raises(csa.CsaError, match="workspace"):
+        csa._expect_workspace("hca_shared_attend", torch.empty(4096, dtype=torch.uint8), torch.device("cuda:0"))
+    with pytest.raises(csa.CsaError, match="workspace"):
+        csa._expect_workspace("hca_shared_attend", torch.empty(64, 64, dtype=torch.uint8).t()[:9], torch.device("cpu"))
