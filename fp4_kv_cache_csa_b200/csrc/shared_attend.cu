@@ -23,22 +23,25 @@
 // rounded to fp16's 11 bits, which leaves about 1e-4 of the output's norm, an order
 // below the bf16 rounding of the output. Row sums, references and accumulators are float32.
 //
-// Warp roles (17 warps, one CTA per SM): eight dequantize (they also bring the
-// group's queries in), eight do the softmax and the outputs, one thread issues the
-// MMAs. At D = 512 a tile of E' takes 128 KB of shared memory, which leaves no room for a
-// second one, and O^T needs it as long as its product runs. So S^T of the next tile takes
-// its E' from tensor memory instead: four of the dequantizing warps write it there part
-// by part (128 channels, two buffers), the other four dequantize the same tile again into
-// shared memory as O^T releases its parts; S^T, softmax and O^T of neighbouring tiles then
-// overlap (one tile after the other, converted once: 1.70 ms; this: 1.64 ms at 512 x 64 heads
-// over 16384 blocks). At D = 128 three tiles fit shared memory and both products read them there.
+// Warp roles (20 warps, one CTA per SM): eight dequantize (they also bring the group's queries in), eight do the
+// softmax and the outputs, two prepare the rows' exponents and scale factors a tile ahead, one thread each issues
+// the MMAs of S^T and of O^T. At D = 512 a tile of E' takes 128 KB of shared memory, which leaves no room for a
+// second one: a part (128 channels) of the next tile is dequantized as soon as O^T has read that part of this one,
+// and S^T follows part by part. At D = 128 three tiles fit.
 //
-// What bounds it: an MMA of M = 128, N = 64, K = 16 takes 48 cycles here with A in shared
-// memory (4 KB at about 90 B/cycle; N = 32 takes as long) against 32 at the tensor rate, so O^T
-// and S^T take about 3000 cycles of a tile; 128 x 64 exponentials 512 cycles of the
-// special-function units; and each conversion of the tile about 2000 warp instructions.
-// Measured, a tile of 64 columns takes about 6500 cycles: the conversions' instruction
-// issue bounds it, then the softmax between the two products.
+// What bounds it: the chain S^T -> softmax -> O^T -> dequantization of the freed parts. Measured at D = 512, 64
+// heads: a tile of 64 columns takes about 5600 cycles, of which S^T's last part 420, the softmax to the last warp's
+// P' 1950 (512 of them exponentials, at 16 a cycle), O^T's first part 500 and the dequantization of two parts by
+// each team 2100, with a few hundred for each hand-over. An MMA of M = 128, N = 64, K = 16 takes 48 cycles here
+// (A's 4 KB from shared memory) against 32 at the tensor rate, so the products alone would take 3000.
+// 512 queries x 64 heads over 16384 blocks, causal: 1.43 ms, 0.77 PFLOP/s.
+//
+// Three things that mattered more than the count of instructions. (1) The roles' loops share an instruction cache
+// that they overflow easily, and misses then go to one that all SMs of a GPC share: with E' of S^T passed through
+// tensor memory instead (dequantized twice, so that S^T runs beside O^T) the loops came to 47 KB, 140 lines a tile
+// missed, and a tile took 6500 cycles although less of it was serial (1.58 ms). (2) With the carve-out at its
+// largest every spilled register is a trip to L2 (see keep_registers). (3) O^T's 32 MMAs in one straight run go out
+// every 48 cycles; a barrier and a fence between the parts, all of them long ready, made it 75 (1.61 ms).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -55,9 +58,10 @@ constexpr int kTile = 128;  // blocks of a tile
 constexpr int kCols = 64;   // columns of a group
 constexpr int kSoftmaxWarps = 8, kDequantWarps = 8;  // the latter in two teams of four
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kDequantWarps + 1);
+constexpr int kThreads = 32 * (kSoftmaxWarps + kDequantWarps + 4);  // whole groups of four, which registers are split by
 constexpr int kTeamWarps = 4;
-constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
+constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;  // S^T; the one behind it: O^T
+constexpr int kFactorWarp = kMmaWarp + 2, kFactorWarps = 2;
 // Row exponents count from B, the largest of the group's first tile in the CTA (127, that is 1, when
 // its rows are all zero). fp16 holds a row of 2^(B - 10) .. 2^(B + 12) exactly without an exponent of its own
 // (groups down to 2^-13 of the row's largest, which a row at B has down to 2^-23), and then takes none: R = 0. Others
@@ -69,7 +73,7 @@ constexpr int kExponentSpan = 40, kEvenBelow = 10, kEvenAbove = 12;
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
 // Calls of up to so many groups and slots are planned in shared memory (2.5 instead of 5.6 us; planned by every CTA of
-// the main kernel for itself, a launch less, they made that kernel's registers spill: 94 -> 106 us at 32 queries).
+// the main kernel for itself, a launch less, they made that kernel's registers spill: 94 -> 106 us at 32 queries then).
 constexpr int kSmallGroups = 512;
 constexpr int kMostCtas = 256;
 
@@ -83,13 +87,12 @@ struct Cfg {
     static constexpr int P_BYTES = kTile * kCols * 2;
     static constexpr int SLICE = kTile * 128;            // 64 channels of a tile
     static constexpr int QSLICE = kCols * 128;           // 64 channels of the queries
-    // D = 512: the blocks' operand of S^T comes through tensor memory, part by part (see the top)
-    static constexpr bool THROUGH_TMEM = D == 512;
-    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T, then two parts of E'
-    static constexpr int TMEM_E = TMEM_O + PARTS * kCols;
-    static constexpr int TMEM_COLS = TMEM_E + (THROUGH_TMEM ? 2 * kCols : 0) <= 256 ? 256 : 512;
+    static constexpr int TMEM_O = 2 * kCols;             // S^T twice, then O^T
+    static constexpr int TMEM_COLS = TMEM_O + PARTS * kCols <= 256 ? 256 : 512;
     static constexpr int MISC = 6144;
-    static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + MISC;
+    static constexpr int FAC_ROW = D / 16;               // bytes of a row's factors
+    static constexpr int FAC_BYTES = kTile * FAC_ROW;    // of a tile; two of them
+    static constexpr int SMEM = 1024 + NBUF * E_BYTES + Q_BYTES + NP * P_BYTES + 2 * FAC_BYTES + MISC;
 };
 
 // A group of columns: queries q0 .. q0 + nq - 1 of slot b, its tiles t0 .. t0 + tiles - 1 of the flat list.
@@ -292,11 +295,6 @@ __global__ void __launch_bounds__(1024) shared_schedule_kernel(SharedArgs a) {
 // ---------------------------------------------------------------- operands
 // Four neighbouring lanes share a row: lane v of them takes its 32-channel group v of every part (128 channels,
 // 64 bytes of codes), so that a warp's 16-byte load covers whole 64-byte pieces of eight rows.
-// Scale words: E8M0, one word per part: lane v holds the word of part v (D = 512) or the row's only one;
-// E4M3, two words per part: likewise.
-struct Scales {
-    uint32_t x, y;
-};
 
 // A load that is issued where it stands (left to itself it is moved down to its use, a part later).
 __device__ __forceinline__ uint4 load_here(const uint8_t *p) {
@@ -311,14 +309,6 @@ __device__ __forceinline__ uint32_t load_word(const uint8_t *p) {
     return r;
 }
 
-// The largest byte of a row's scale words.
-__device__ __forceinline__ int row_exponent(uint32_t word) {
-    uint32_t m = __vmaxu4(word, word >> 16);
-    m = max(m & 0xFF, (m >> 8) & 0xFF);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return (int)max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-}
-
 // Eight E2M1 codes to four fp16 pairs. (One conversion takes any byte of a register as it is; the header's
 // function for a byte value first cuts it out: 8 instead of about 14 instructions a word with the scaling.)
 __device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&o)[4]) {
@@ -331,33 +321,33 @@ __device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&o)[4]) {
 
 // Where a part's 16 chunks of 8 channels go: chunk 4 v + k (lane v's word k) becomes chunk 8 (k / 2) + 2 v + k % 2, so
 // that for every k the eight lanes of two rows store to eight different banks. Outputs are read back through
-// channel_at, and where S^T takes its blocks from the same tile (D = 128) the queries follow in the same order.
+// channel_at, and the queries follow in the same order.
 __device__ __forceinline__ int chunk_place(int kc) { return 8 * ((kc >> 1) & 1) + 2 * (kc >> 2) + (kc & 1); }
 __device__ __forceinline__ int channel_at(int pos) {  // of a part's position
     const int pc = pos >> 3;
     return 8 * (4 * ((pc & 7) >> 1) + 2 * (pc >> 3) + (pc & 1)) + (pos & 7);
 }
 
-// The factors of a lane's 32 channels of one part of a row, as fp16 pairs: of words 0 and 1, and of 2 and 3.
+// The factors of a lane's 32 channels of one part of a row, as fp16 pairs: of words 0 and 1, and of 2 and 3. f: the
+// factor warps' 16 bits, twice.
 template <int SF>
-__device__ __forceinline__ void scale_halves(Scales sc, int rmax, int v, uint32_t (&s2)[2]) {
+__device__ __forceinline__ void scale_halves(uint32_t f, uint32_t (&s2)[2]) {
     if constexpr (SF == kScaleE8M0x32) {
-        // 2^(X - rmax) from a float32 with that exponent (fp16 rounds what lies below 2^-25 to zero)
-        const int e = max((int)((sc.x >> (8 * v)) & 0xFF) - rmax + 127, 0);
-        const float f = __uint_as_float((uint32_t)e << 23);
-        const __half2 h = __floats2half2_rn(f, f);
-        s2[0] = s2[1] = *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        // E' = e 2^-7
-        const uint32_t bytes = ((v & 2) ? sc.y : sc.x) >> (16 * (v & 1));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)((bytes >> (8 * h)) & 0xFF), __NV_E4M3);
-            const __half x = __hmul(__half(hr), __ushort_as_half((uint16_t)((15 - 7) << 10)));
-            const __half2 x2 = __halves2half2(x, x);
-            s2[h] = *reinterpret_cast<const uint32_t *>(&x2);
-        }
+        s2[0] = s2[1] = f;
+    } else {  // two scales, E' = e 2^-7
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(f & 0xFFFF), __NV_E4M3);
+        const __half2 x = __hmul2(__half2(h), __halves2half2(__ushort_as_half((15 - 7) << 10), __ushort_as_half((15 - 7) << 10)));
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&x);
+        s2[0] = __byte_perm(w, 0, 0x1010);
+        s2[1] = __byte_perm(w, 0, 0x3232);
     }
+}
+
+// 2^(X - R) of the bytes `at` of two words, as a pair of fp16 (which rounds what lies below 2^-25 to zero).
+__device__ __forceinline__ uint32_t factor_pair(uint32_t lo, uint32_t hi, int at, int R) {
+    const int x = max((int)((lo >> (8 * at)) & 0xFF) - R + 127, 0), y = max((int)((hi >> (8 * at)) & 0xFF) - R + 127, 0);
+    const __half2 h = __floats2half2_rn(__uint_as_float((uint32_t)x << 23), __uint_as_float((uint32_t)y << 23));
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Sixteen codes to eight fp16 pairs.
@@ -377,9 +367,9 @@ __device__ __forceinline__ void scaled_halves(uint32_t w0, uint32_t w1, uint32_t
 // Row 32 dw + rl + 8 I of a part into its place in the 128-byte-swizzled tile in shared memory. to0, to1: the places of
 // words 0 and 1 of row 32 dw + rl; words 2 and 3 lie a slice further on.
 template <int SF, int I, int SLICE>
-__device__ __forceinline__ void dequant_smem(const uint4 &code, Scales sc, int rmax, int v, uint32_t to0, uint32_t to1) {
+__device__ __forceinline__ void dequant_smem(const uint4 &code, uint32_t f, uint32_t to0, uint32_t to1) {
     uint32_t s2[2], o[8];
-    scale_halves<SF>(sc, rmax, v, s2);
+    scale_halves<SF>(f, s2);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         scaled_halves(k ? code.z : code.x, k ? code.w : code.y, s2[k], o);
@@ -391,22 +381,10 @@ __device__ __forceinline__ void dequant_smem(const uint4 &code, Scales sc, int r
     }
 }
 
-// Sixteen rows of half a part into tensor memory (32 columns of fp16 pairs): a is row lane / 4, b row lane / 4 + 8. Pair m
-// of lane v goes to column 8 (m / 2) + 2 v + m % 2 (the fragment of a 16x256b store), so channel 32 v + 2 m + e of
-// the part is the MMA's k = 16 (m / 2) + 4 v + 2 (m % 2) + e.
-__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&a)[8], const uint32_t (&b)[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
-            taddr),
-        "r"(a[0]), "r"(a[1]), "r"(b[0]), "r"(b[1]), "r"(a[2]), "r"(a[3]), "r"(b[2]), "r"(b[3]), "r"(a[4]), "r"(a[5]),
-        "r"(b[4]), "r"(b[5]), "r"(a[6]), "r"(a[7]), "r"(b[6]), "r"(b[7])
-        : "memory");
-}
-
 // ---------------------------------------------------------------- main kernel
-// 17 warps leave 96 registers a thread. Saying so at the start of a role changes no split, but makes the compiler
+// 20 warps leave 96 registers a thread. Saying so at the start of a role changes no split, but makes the compiler
 // allocate the role by itself: without it values that only rare paths need are spilled around the tile loop, and
-// with nearly all of L1 taken as shared memory every reload is a trip to L2 (2.2 ms against 1.64
+// with nearly all of L1 taken as shared memory every reload is a trip to L2 (2.2 ms against 1.64 when it was added,
 // at D = 512, 512 x 64 heads over 16384 blocks).
 __device__ __forceinline__ void keep_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
 
@@ -452,19 +430,6 @@ __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity, const
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return done || mbar_wait_ab<false>(smem_u32(bar), parity, abort);
-}
-
-// Whether a barrier's phase is complete, without waiting.
-__device__ __forceinline__ bool is_done(const uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
 }
 
 // One lane of the warp, the same one every time (the compiler then knows that a single thread runs).
@@ -523,23 +488,9 @@ __device__ __forceinline__ void reduce_columns(float2 (&v)[8]) {
     }
 }
 
-// ... with A (fp16 pairs) in tensor memory.
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-        "mov.b64 b, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n"
-        :
-        : "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
-
-// B + 127 from what the dequantizing warps found (E8M0).
-__device__ __forceinline__ int base_of(const int (&b)[kTeamWarps]) {
-    int m = b[0];
-#pragma unroll
-    for (int k = 1; k < kTeamWarps; ++k) m = max(m, b[k]);
+// B + 127 from what the factor warps found (E8M0).
+__device__ __forceinline__ int base_of(const int (&b)[kFactorWarps]) {
+    const int m = max(b[0], b[1]);
     return m > 0 ? m : 127;
 }
 
@@ -571,16 +522,16 @@ struct Cursor {
 
 // Shared state behind the operand buffers.
 struct Misc {
-    uint64_t e_full[3][4], e_free[3][4], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free[2], r_full, drain;
-    uint64_t a_full[2], a_free[2], x_full[2];
+    uint64_t e_full[3][4], e_free[3][4], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free[2], r_full[2], drain[2];
+    uint64_t f_full[2];
     uint32_t tmem;
     int abort;
     alignas(16) float minus_rho[kCols], alpha[kCols], fac[kCols], jfac[kCols];
     float wred[kSoftmaxWarps][kCols];
     float colmul[2][kCols];  // scale_log2 * 2^(sQ + B) of each column, by segment parity
     int nvis[2][kCols];
-    float rexp[3][kTile];    // R_j - B
-    int base[2][4];          // largest exponent byte of each dequantizing warp's rows, by segment parity
+    float rexp[2][kTile];    // R_j - B
+    int base[2][kFactorWarps];  // largest exponent byte of each factor warp's rows, by segment parity
 };
 static_assert(sizeof(Misc) <= 6144, "Misc exceeds its space");
 
@@ -592,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     uint8_t *E = smem;
     uint8_t *Q = E + C::NBUF * C::E_BYTES;
     uint8_t *P = Q + C::Q_BYTES;
-    Misc *ms = reinterpret_cast<Misc *>(P + C::NP * C::P_BYTES);
+    uint8_t *fac = P + C::NP * C::P_BYTES;
+    Misc *ms = reinterpret_cast<Misc *>(fac + 2 * C::FAC_BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < C::NBUF; ++b)
@@ -606,14 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             mbar_init(smem_u32(&ms->p_full[b]), kSoftmaxWarps);
             mbar_init(smem_u32(&ms->pv_done[b]), 1);
             mbar_init(smem_u32(&ms->o_free[b]), kSoftmaxWarps);
-            mbar_init(smem_u32(&ms->a_full[b]), kTeamWarps);
-            mbar_init(smem_u32(&ms->a_free[b]), 1);
-            mbar_init(smem_u32(&ms->x_full[b]), kTeamWarps);
+            mbar_init(smem_u32(&ms->f_full[b]), kFactorWarps);
+            mbar_init(smem_u32(&ms->r_full[b]), kFactorWarps);
+            mbar_init(smem_u32(&ms->drain[b]), 1);
         }
         mbar_init(smem_u32(&ms->q_full), kDequantWarps);
-        mbar_init(smem_u32(&ms->r_full), kTeamWarps);
         mbar_init(smem_u32(&ms->q_free), 1);
-        mbar_init(smem_u32(&ms->drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ms->abort = 0;
     }
@@ -685,11 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
             for (int b = 0; b < 8; ++b) lsum[b] = make_float2(0.f, 0.f);
             while (true) {
                 const bool first = c.first;
-                const int buf = n % C::NBUF, sb = n & 1, use = n / C::NBUF;
+                const int sb = n & 1;
                 // the rows' exponents from B on: 0 for almost all of them
-                const int xb = C::THROUGH_TMEM ? sb : buf;
-                ok = ok && (C::THROUGH_TMEM ? wait(&ms->x_full[sb], (n >> 1) & 1, abort) : wait(&ms->e_full[buf][0], use & 1, abort));
-                const float R0 = ms->rexp[xb][r0], R1 = ms->rexp[xb][r0 + 8];
+                ok = ok && wait(&ms->f_full[sb], (n >> 1) & 1, abort);
+                const float R0 = ms->rexp[sb][r0], R1 = ms->rexp[sb][r0 + 8];
                 const bool even = !__any_sync(0xffffffffu, R0 != 0.f || R1 != 0.f);
                 const bool masked = (c.lt + 1) * kTile > n_min;
                 ok = ok && wait(&ms->s_full[sb], (n >> 1) & 1, abort);
@@ -743,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                         for (int k = 0; k < 32; ++k) u[k] = u[k] > 8.f ? 8.f : u[k];
                     }
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) over = fmaxf(over, u[k]);
+                    for (int k = 0; k < 8; ++k) over = fmaxf(over, fmaxf(fmaxf(u[k], u[k + 8]), fmaxf(u[k + 16], u[k + 24])));
                     const bool set = first && pass == 0;
                     if (!bar_or_n<kSoftmaxThreads>(set || over > 8.f || !ok)) break;
                     if (!first) ok = ok && wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
@@ -905,19 +854,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
     } else if (warp < kMmaWarp) {
         // ================================================================ dequantization, queries
         keep_registers();
-        // Two teams of four warps. D = 512: the first brings every tile's parts into tensor memory for S^T, the second
-        // into shared memory for O^T, a tile later. D = 128: every other tile into shared memory, for both.
+        // Two teams of four warps. D = 512: each takes every other part of a tile; D = 128: every other tile.
         const int dw = warp & 3, team = (warp - kSoftmaxWarps) >> 2, v = lane & 3, rl = lane >> 2;
         // this lane's rows of a tile are 32 dw + rl + 8 i, i = 0 .. 3
         const int j = 32 * dw + rl;
-        const uint32_t place = smem_u32(E) + dw * 4096 + rl * 128;
+        const uint32_t place = smem_u32(E) + j * 128;
         const uint32_t off0 = place + (((2 * v) ^ rl) << 4), off1 = place + (((2 * v + 1) ^ rl) << 4);
-        // parts ahead in registers
-        constexpr int MINE = D == 512 ? 2 : 1;
+        constexpr int MINE = D == 512 ? 2 : 1;  // parts of a team; their codes of the team's next tile wait in registers
         Cursor c = start();
         int slot_g = c.g, slot = a.groups[c.g].b, n_max = a.groups[c.g].n_max;  // the group of the rows asked for last
         uint4 code[MINE][4];
-        Scales sc[4], nsc[4];
         // this lane's first row of a tile (its codes of part 0), and how many rows from there on are visible
         // (the others are zero codes)
         struct Rows {
@@ -938,45 +884,22 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
         };
         // (rows behind the last visible one load that one again; their factors are 0)
         auto load_codes = [&](uint4 (&to)[4], const uint8_t *src, int live) {
-            if (live >= 32 - rl) {  // the warp's 32 rows are all visible
 #pragma unroll
-                for (int i = 0; i < 4; ++i) to[i] = load_here(src + i * 8 * (D / 2));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) to[i] = load_here(src + (min(8 * i, live - 1) * (D / 2)));
-            }
+            for (int i = 0; i < 4; ++i) to[i] = load_here(src + min(8 * i, live - 1) * (D / 2));
         };
-        auto load_tile_scales = [&](Scales (&to)[4], const Rows &r) {  // of the group that rows_of went to last
-            constexpr int BYTES = 4 * (SF == kScaleE4M3x16 ? 2 : 1) * C::PARTS;  // of a row
-            const uint8_t *src = a.scale + ((size_t)slot * a.cap + (n_max - r.live)) * BYTES + (D == 512 ? BYTES / 4 * v : 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                to[i].x = to[i].y = 0;
-                if (8 * i < r.live) {
-                    to[i].x = load_word(src + 8 * i * BYTES);
-                    if constexpr (SF == kScaleE4M3x16) to[i].y = load_word(src + 8 * i * BYTES + 4);
-                }
-            }
+        auto part = [&](int m) { return D == 512 ? team + 2 * m : 0; };
+        auto load_part = [&](int m, const Rows &r) {  // (nothing of a group without visible blocks, or behind the last tile)
+            if (r.codes && n_max > 0) load_codes(code[m], r.codes + part(m) * 64, r.live);
         };
-        Rows rows = {};  // of the tile that code and sc hold
 #pragma unroll
-        for (int m = 0; m < MINE; ++m)
+        for (int m = 0; m < MINE; ++m) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) code[m][i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i].x = sc[i].y = nsc[i].x = nsc[i].y = 0;
-        {
             Cursor x = c;
             if (D == 128 && team == 1) step(x);
-            if (x.left > 0) {
-                rows = rows_of(x);
-#pragma unroll
-                for (int m = 0; m < MINE; ++m)
-                    if (n_max > 0) load_codes(code[m], rows.codes + m * 64, rows.live);
-                load_tile_scales(sc, rows);
-            }
+            if (x.left > 0) load_part(m, rows_of(x));
         }
-        int n = 0, base = 127 + 7;
+        int n = 0;
         bool ok = true;
         while (c.left > 0) {
             if (c.first) {
@@ -986,18 +909,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 if (c.seg >= 2) ok = ok && wait(&ms->o_free[c.seg & 1], ((c.seg - 2) >> 1) & 1, abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const int cols = gr.nq * a.H, mp = c.seg & 1;
-                if constexpr (SF == kScaleE8M0x32) {  // B, from the rows of the group's first tile
-                    if (team == (D == 512 ? 0 : n & 1)) {
-                        int mine = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mine = max(mine, row_exponent(sc[i].x));
-                        mine = __reduce_max_sync(0xffffffffu, mine);
-                        if (lane == 0) {
-                            ms->base[mp][dw] = mine;
-                            mbar_arrive(smem_u32(&ms->r_full));
-                        }
-                    }
-                    ok = wait(&ms->r_full, c.seg & 1, abort);
+                int base = 127 + 7;
+                if constexpr (SF == kScaleE8M0x32) {
+                    ok = wait(&ms->r_full[mp], (c.seg >> 1) & 1, abort);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     base = base_of(ms->base[mp]);
                 }
@@ -1043,21 +957,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                                 const __half2 hh = __floats2half2_rn(f.x * inv, f.y * inv);
                                 o[z] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
-                            if constexpr (C::THROUGH_TMEM) {
-                                // the k order of tmem_st_rows: two 8-byte pieces, k = 16 x + 4 w .. + 3
-                                const int w = (kc & 15) >> 2;
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) {
-                                    const int x = 2 * (kc & 3) + z;
-                                    *reinterpret_cast<uint2 *>(Q + (2 * (kc >> 4) + (x >> 2)) * C::QSLICE + (col >> 3) * 1024 +
-                                                               (col & 7) * 128 + (((2 * (x & 3) + (w >> 1)) ^ (col & 7)) << 4) +
-                                                               8 * (w & 1)) = make_uint2(o[2 * z], o[2 * z + 1]);
-                                }
-                            } else {
-                                const int pc = chunk_place(kc);
-                                *reinterpret_cast<uint4 *>(Q + (pc >> 3) * C::QSLICE + (col >> 3) * 1024 + (col & 7) * 128 +
-                                                           (((pc & 7) ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                            const int pc = (kc & ~15) + chunk_place(kc & 15);
+                            *reinterpret_cast<uint4 *>(Q + (pc >> 3) * C::QSLICE + (col >> 3) * 1024 + (col & 7) * 128 +
+                                                       (((pc & 7) ^ (col & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                         if (sl == 0) {
                             ms->colmul[mp][col] = ldexpf(a.scale_log2, sq + base - 127);
@@ -1070,216 +972,223 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
             }
             const int buf = n % C::NBUF, use = n / C::NBUF;
-            auto words = [&](int i, int p) {
-                Scales x = sc[i];
-                if constexpr (D == 512) {  // part p's words are lane p's of the four
-                    x.x = __shfl_sync(0xffffffffu, x.x, (lane & ~3) | p);
-                    if constexpr (SF == kScaleE4M3x16) x.y = __shfl_sync(0xffffffffu, x.y, (lane & ~3) | p);
-                }
-                return x;
-            };
-            // one part into its place in shared memory, and the codes of the part at `then` on their way
-            auto to_smem = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const uint8_t *then, int live) {
+            if (D == 128 && (n & 1) != team) {
+                step(c);
+                ++n;
+                continue;
+            }
+            // this lane's factors of the tile: 16 bits for each part
+            uint2 f[4];
+            ok = wait(&ms->f_full[n & 1], (n >> 1) & 1, abort) && ok;
+            const uint8_t *src = fac + (n & 1) * C::FAC_BYTES + j * C::FAC_ROW + v * (C::FAC_ROW / 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (D == 512) f[i] = *reinterpret_cast<const uint2 *>(src + 8 * i * C::FAC_ROW);
+                else f[i].x = *reinterpret_cast<const uint16_t *>(src + 8 * i * C::FAC_ROW);
+            }
+            step(c);
+            Cursor x = c;  // the team's next tile
+            if (D == 128 && x.left > 0) step(x);
+            Rows rows = {};
+            if (x.left > 0) rows = rows_of(x);
+#pragma unroll
+            for (int m = 0; m < MINE; ++m) {
+                const int p = part(m);
                 if (use >= 1) ok = wait(&ms->e_free[buf][p], (use - 1) & 1, abort) && ok;
                 const uint32_t at = buf * C::E_BYTES + p * (2 * C::SLICE);
-                dequant_smem<SF, 0, C::SLICE>(from[0], words(0, p), rmax[0], v, off0 + at, off1 + at);
-                dequant_smem<SF, 1, C::SLICE>(from[1], words(1, p), rmax[1], v, off0 + at, off1 + at);
-                dequant_smem<SF, 2, C::SLICE>(from[2], words(2, p), rmax[2], v, off0 + at, off1 + at);
-                dequant_smem<SF, 3, C::SLICE>(from[3], words(3, p), rmax[3], v, off0 + at, off1 + at);
+                auto factor = [&](int i) { return __byte_perm(p & 2 ? f[i].y : f[i].x, 0, p & 1 ? 0x3232 : 0x1010); };
+                dequant_smem<SF, 0, C::SLICE>(code[m][0], factor(0), off0 + at, off1 + at);
+                dequant_smem<SF, 1, C::SLICE>(code[m][1], factor(1), off0 + at, off1 + at);
+                dequant_smem<SF, 2, C::SLICE>(code[m][2], factor(2), off0 + at, off1 + at);
+                dequant_smem<SF, 3, C::SLICE>(code[m][3], factor(3), off0 + at, off1 + at);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms->e_full[buf][p]));
-                if (then) load_codes(from, then, live);
-            };
-            // ... into tensor memory
-            auto to_tmem = [&](uint4 (&from)[4], int p, const int (&rmax)[4], const uint8_t *then, int live) {
-                // parts alternate between two buffers: this is use 2 n + p / 2 of its one
-                if (n >= 1 || p >= 2) ok = wait(&ms->a_free[p & 1], ((p >> 1) ^ 1) & 1, abort) && ok;
-                tc_fence_after();
-                const uint32_t at = tmem + C::TMEM_E + kCols * (p & 1) + ((uint32_t)(32 * dw) << 16);
+                load_part(m, rows);
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+            ++n;
+        }
+        if (!ok) ms->abort = 1;
+    } else {
+        keep_registers();
+        if (warp >= kFactorWarp) {
+            // ================================================================ scales
+            // The tiles' scales, a row a lane: the rows' exponents R, and each group's factor (E4M3: its byte) where the lane
+            // that dequantizes it finds those of all parts together: 16 bits at [row][v][part]. In warps of their own
+            // they keep that work, and its registers, out of the dequantizing warps' loop.
+            constexpr int W = D / (SF == kScaleE4M3x16 ? 64 : 128);  // words of a row's scales
+            const int row0 = 64 * (warp - kFactorWarp) + lane;  // and row0 + 32
+            Cursor c = start();
+            int n = 0, base = 127 + 7;
+            bool ok = true;
+            while (c.left > 0) {
+                const int b = a.groups[c.g].b, n_max = a.groups[c.g].n_max;
+                uint32_t w[2][W];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t sx[2], sy[2], x[8], y[8];
-                    scale_halves<SF>(words(2 * h, p), rmax[2 * h], v, sx);
-                    scale_halves<SF>(words(2 * h + 1, p), rmax[2 * h + 1], v, sy);
-                    const uint32_t to = at + ((uint32_t)(16 * h) << 16);
-                    scaled_halves(from[2 * h].x, from[2 * h].y, sx[0], x);
-                    scaled_halves(from[2 * h + 1].x, from[2 * h + 1].y, sy[0], y);
-                    tmem_st_rows(to, x, y);
-                    scaled_halves(from[2 * h].z, from[2 * h].w, sx[1], x);
-                    scaled_halves(from[2 * h + 1].z, from[2 * h + 1].w, sy[1], y);
-                    tmem_st_rows(to + 32, x, y);
-                }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms->a_full[p & 1]));
-                if (then) load_codes(from, then, live);
-            };
-            auto post_exponents = [&](const int (&rmax)[4], int where) {
-                if (v == 0) {
+                for (int k = 0; k < 2; ++k) {
+                    const int e = c.lt * kTile + row0 + 32 * k;
+                    const uint8_t *src = a.scale + ((size_t)b * a.cap + e) * (4 * W);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ms->rexp[where][j + 8 * i] = rmax[i] == kNoRow ? 0.f : (float)(rmax[i] - base);
-                }
-            };
-            auto exponents = [&](int (&rmax)[4]) {
+                    for (int x = 0; x < W; x += 4) {
+                        if constexpr (W >= 4) {
+                            const uint4 u = e < n_max ? load_here(src + 4 * x) : make_uint4(0, 0, 0, 0);
+                            w[k][x] = u.x;
+                            w[k][x + 1] = u.y;
+                            w[k][x + 2] = u.z;
+                            w[k][x + 3] = u.w;
+                        } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    rmax[i] = base;
-                    if constexpr (SF == kScaleE8M0x32) {
-                        const int m = row_exponent(sc[i].x), d = m - base;
-                        if (d < -kEvenBelow || d > kEvenAbove) rmax[i] = max(m, base - kExponentSpan);
-                        if (8 * i >= rows.live) rmax[i] = kNoRow;
+                            for (int y = 0; y < W; ++y) w[k][y] = e < n_max ? load_word(src + 4 * y) : 0;
+                        }
                     }
                 }
-            };
-            if constexpr (D == 512) {
-                int rmax[4];
-                exponents(rmax);
-                step(c);
-                if (team == 0) {
-                    if (n >= 2) ok = wait(&ms->s_free[n & 1], ((n >> 1) - 1) & 1, abort) && ok;  // rexp is read, too
-                    post_exponents(rmax, n & 1);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&ms->x_full[n & 1]));
-                }
-#pragma unroll 1
-                for (int p = 0; p < C::PARTS; p += 2) {
-                    if (p == 2) {  // from here on the next tile's codes are loaded
-                        rows = {};
-                        if (c.left > 0) rows = rows_of(c);
-                        load_tile_scales(nsc, rows);
+                // the exponents and factors of tile n - 2 are read: its S^T, which takes all of its dequantized rows, is, too
+                if (n >= 2) ok = wait(&ms->s_free[n & 1], ((n >> 1) - 1) & 1, abort) && ok;
+                int m[2];  // the rows' largest exponents
+                if constexpr (SF == kScaleE8M0x32) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x = w[k][0];
+#pragma unroll
+                        for (int y = 1; y < W; ++y) x = __vmaxu4(x, w[k][y]);
+                        x = __vmaxu4(x, x >> 16);
+                        m[k] = (int)max(x & 0xFF, (x >> 8) & 0xFF);
                     }
-                    // (no codes to load behind the last tile, and of a group without visible blocks)
-                    const uint8_t *then = rows.codes && n_max > 0 ? rows.codes + (p ^ 2) * 64 : nullptr;
-                    const uint8_t *then1 = then ? then + 64 : nullptr;
-                    if (team == 0) {
-                        to_tmem(code[0], p, rmax, then, rows.live);
-                        to_tmem(code[1], p + 1, rmax, then1, rows.live);
-                    } else {
-                        to_smem(code[0], p, rmax, then, rows.live);
-                        to_smem(code[1], p + 1, rmax, then1, rows.live);
+                    if (c.first) {  // B
+                        if (c.seg >= 2) ok = wait(&ms->o_free[c.seg & 1], ((c.seg - 2) >> 1) & 1, abort) && ok;
+                        const int mine = __reduce_max_sync(0xffffffffu, max(m[0], m[1]));
+                        if (lane == 0) {
+                            ms->base[c.seg & 1][warp - kFactorWarp] = mine;
+                            mbar_arrive(smem_u32(&ms->r_full[c.seg & 1]));
+                        }
+                        ok = wait(&ms->r_full[c.seg & 1], (c.seg >> 1) & 1, abort) && ok;
+                        base = base_of(ms->base[c.seg & 1]);
                     }
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
-            } else {
-                if ((n & 1) == team) {
-                    int rmax[4];
-                    exponents(rmax);
-                    if (use >= 1) ok = wait(&ms->e_free[buf][0], (use - 1) & 1, abort) && ok;
-                    post_exponents(rmax, buf);
-                    Cursor x = c;
-                    step(x);
-                    if (x.left > 0) step(x);
-                    rows = {};
-                    if (x.left > 0) rows = rows_of(x);
-                    load_tile_scales(nsc, rows);
-                    to_smem(code[0], 0, rmax, n_max > 0 ? rows.codes : nullptr, rows.live);
-                    if (!__all_sync(0xffffffffu, ok)) break;
+                for (int k = 0; k < 2; ++k) {
+                    const int row = row0 + 32 * k;
+                    uint32_t o[D == 512 ? 8 : 2];
+                    int R = base;
+                    if constexpr (SF == kScaleE8M0x32) {
+                        const int d = m[k] - base;
+                        if (d < -kEvenBelow || d > kEvenAbove) R = max(m[k], base - kExponentSpan);
+                        const bool live = c.lt * kTile + row < n_max;
+                        ms->rexp[n & 1][row] = live ? (float)(R - base) : 0.f;
+                        if (!live) R = kNoRow;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[i] = nsc[i];
+                        for (int v = 0; v < 4; ++v) {
+                            if constexpr (D == 512) {
+                                o[2 * v] = factor_pair(w[k][0], w[k][1], v, R);
+                                o[2 * v + 1] = factor_pair(w[k][2], w[k][3], v, R);
+                            } else if (v % 2 == 0) {
+                                o[v / 2] = factor_pair(w[k][0] >> (8 * v), w[k][0] >> (8 * v + 8), 0, R);
+                            }
+                        }
+                    } else {
+                        ms->rexp[n & 1][row] = 0.f;
+                        if constexpr (D == 512) {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const uint32_t pick = v & 1 ? 0x7632 : 0x5410;
+                                o[2 * v] = __byte_perm(w[k][v >> 1], w[k][2 + (v >> 1)], pick);
+                                o[2 * v + 1] = __byte_perm(w[k][4 + (v >> 1)], w[k][6 + (v >> 1)], pick);
+                            }
+                        } else {
+                            o[0] = w[k][0];
+                            o[1] = w[k][1];
+                        }
+                    }
+                    uint8_t *dst = fac + (n & 1) * C::FAC_BYTES + row * C::FAC_ROW;
+                    if constexpr (D == 512) {
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else {
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(o[0], o[1]);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms->f_full[n & 1]));
                 step(c);
+                ++n;
             }
-            ++n;
-        }
-        if (!ok) ms->abort = 1;
-    } else if (elect_one()) {  // (the warp's other lanes wait at the common end)
-        // ================================================================ MMA issue
-        constexpr uint32_t IDESC_S = idesc_f16(kTile, kCols, false, false);
-        constexpr uint32_t IDESC_O = idesc_f16(kTile, kCols, true, true);
-        // operand descriptors: E' and Q' by channels (S^T), E' and P' by blocks (O^T); 16 bytes a unit
-        const uint64_t de = desc_sw128(smem_u32(E), 16, 1024), dq = desc_sw128(smem_u32(Q), 16, 1024);
-        const uint64_t dv = desc_sw128(smem_u32(E), C::SLICE, 1024), dp = desc_sw128(smem_u32(P), 8192, 1024);
-        const uint32_t e_hi = (uint32_t)(de >> 32), q_hi = (uint32_t)(dq >> 32), v_hi = (uint32_t)(dv >> 32),
-                       p_hi = (uint32_t)(dp >> 32);
-        // Parts of S^T (up to two tiles ahead) and of O^T are issued as their operands become ready, whichever
-        // is: waiting for one of the two in turn held the other up.
-        struct Role {
-            int n, p;           // tile, part of it
-            int g, seg, mine;   // its group, the group's number within the CTA, tiles left of it
-            bool first;         // first tile of the group within the CTA
-        };
-        const int g0 = a.cta_g[blockIdx.x];
-        Role s = {0, 0, g0, 0, min(n_tiles, (int)(a.groups[g0].t0 + a.groups[g0].tiles - t_begin)), true};
-        Role v = s;
-        auto next_tile = [&](Role &r) {
-            r.p = 0;
-            ++r.n;
-            r.first = false;
-            if (--r.mine == 0 && r.n < n_tiles) {
-                ++r.g;
-                ++r.seg;
-                r.mine = min(n_tiles - r.n, a.groups[r.g].tiles);
-                r.first = true;
-            }
-        };
-        bool ok = true;
-        long long since = clock64();
-        while (v.n < n_tiles) {
-            bool moved = false;
-            if (v.n < s.n) {  // O^T += of tile v.n
-                const int buf = v.n % C::NBUF;
-                bool ready = v.p > 0 || (is_done(&ms->p_full[v.n % C::NP], (v.n / C::NP) & 1) &&
-                                         (!v.first || v.seg == 0 || is_done(&ms->o_free[(v.seg - 1) & 1], ((v.seg - 1) >> 1) & 1)));
-                if (C::THROUGH_TMEM && ready) ready = is_done(&ms->e_full[0][v.p], v.n & 1);
-                if (ready) {
-                    tc_fence_after();
-                    const uint32_t a_lo = (uint32_t)dv + ((buf * C::E_BYTES + v.p * 2 * C::SLICE) >> 4);
-                    const uint32_t b_lo = (uint32_t)dp + (v.n % C::NP) * (C::P_BYTES >> 4), d = tmem + C::TMEM_O + kCols * v.p;
+            if (!ok) ms->abort = 1;
+        } else if (elect_one()) {  // (the warp's other lanes wait at the common end)
+            // ================================================================ MMA issue
+            // One warp issues S^T, the other O^T: either product waits for barriers of its own.
+            constexpr uint32_t IDESC_S = idesc_f16(kTile, kCols, false, false);
+            constexpr uint32_t IDESC_O = idesc_f16(kTile, kCols, true, true);
+            const bool scores = warp == kMmaWarp;  // ... and not O^T
+            // its group, the group's number within the CTA, tiles left of it
+            int g = a.cta_g[blockIdx.x], seg = 0;
+            int mine = min(n_tiles, (int)(a.groups[g].t0 + a.groups[g].tiles - t_begin));
+            bool first = true, ok = true;  // first tile of the group within the CTA
+            auto next_tile = [&](int n) {
+                first = false;
+                if (--mine == 0 && n + 1 < n_tiles) {
+                    ++g;
+                    ++seg;
+                    mine = min(n_tiles - n - 1, a.groups[g].tiles);
+                    first = true;
+                }
+            };
+            if (scores) {  // E' and Q' by channels; 16 bytes a unit
+                const uint64_t de = desc_sw128(smem_u32(E), 16, 1024), dq = desc_sw128(smem_u32(Q), 16, 1024);
+                const uint32_t e_hi = (uint32_t)(de >> 32), q_hi = (uint32_t)(dq >> 32);
+                for (int n = 0; n < n_tiles && ok; ++n) {
+                    const int buf = n % C::NBUF, sb = n & 1;
+                    const uint32_t d = tmem + kCols * sb;
+                    if (first) ok = wait(&ms->q_full, seg & 1, abort);
+                    if (n >= 2) ok = ok && wait(&ms->s_free[sb], ((n >> 1) - 1) & 1, abort);
+#pragma unroll 1
+                    for (int p = 0; p < C::PARTS; ++p) {
+                        ok = ok && wait(&ms->e_full[buf][p], (n / C::NBUF) & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a_lo = (uint32_t)de + ((buf * C::E_BYTES + p * 2 * C::SLICE) >> 4);
+                        const uint32_t b_lo = (uint32_t)dq + (p * 2 * C::QSLICE >> 4);
 #pragma unroll
-                    for (int kj = 0; kj < kTile / 16; ++kj)  // 16 blocks each
-                        mma(d, a_lo + (kj * 2048 >> 4), v_hi, b_lo + (kj * 2048 >> 4), p_hi, IDESC_O, kj > 0 || !v.first);
-                    mma_commit(smem_u32(&ms->e_free[buf][v.p]));
-                    if (++v.p == C::PARTS) {
-                        mma_commit(smem_u32(&ms->pv_done[v.n & 1]));
-                        next_tile(v);
+                        for (int kk = 0; kk < 8; ++kk) {  // 16 channels each, 64 of a slice
+                            const uint32_t b_at = b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4);
+                            mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi, b_at, q_hi, IDESC_S, kk > 0 || p > 0);
+                        }
                     }
-                    moved = true;
+                    if (!ok) break;
+                    mma_commit(smem_u32(&ms->s_full[sb]));
+                    if (mine == 1) mma_commit(smem_u32(&ms->q_free));
+                    next_tile(n);
+                }
+            } else {  // E' and P' by blocks
+                const uint64_t dv = desc_sw128(smem_u32(E), C::SLICE, 1024), dp = desc_sw128(smem_u32(P), 8192, 1024);
+                const uint32_t v_hi = (uint32_t)(dv >> 32), p_hi = (uint32_t)(dp >> 32);
+                for (int n = 0; n < n_tiles && ok; ++n) {
+                    const int buf = n % C::NBUF;
+                    const uint32_t b_lo = (uint32_t)dp + (n % C::NP) * (C::P_BYTES >> 4);
+                    ok = wait(&ms->p_full[n % C::NP], (n / C::NP) & 1, abort);
+                    if (first && seg > 0) ok = ok && wait(&ms->o_free[(seg - 1) & 1], ((seg - 1) >> 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int p = 0; p < C::PARTS; ++p) {  // (all parts are there: S^T read them)
+                        const uint32_t a_lo = (uint32_t)dv + ((buf * C::E_BYTES + p * 2 * C::SLICE) >> 4);
+#pragma unroll
+                        for (int kj = 0; kj < kTile / 16; ++kj)  // 16 blocks each
+                            mma(tmem + C::TMEM_O + kCols * p, a_lo + (kj * 2048 >> 4), v_hi, b_lo + (kj * 2048 >> 4), p_hi, IDESC_O,
+                                kj > 0 || !first);
+                        mma_commit(smem_u32(&ms->e_free[buf][p]));
+                    }
+                    mma_commit(smem_u32(&ms->pv_done[n & 1]));
+                    next_tile(n);
                 }
             }
-            if (s.n < n_tiles) {  // S^T of tile s.n
-                const int buf = s.n % C::NBUF, sb = s.n & 1;
-                bool ready = s.p > 0 || ((!s.first || is_done(&ms->q_full, s.seg & 1)) &&
-                                         (s.n < 2 || is_done(&ms->s_free[sb], ((s.n >> 1) - 1) & 1)));
-                // (use 2 n + p / 2 of a part's tensor memory)
-                if (ready) ready = C::THROUGH_TMEM ? is_done(&ms->a_full[s.p & 1], (s.p >> 1) & 1)
-                                                   : is_done(&ms->e_full[buf][s.p], (s.n / C::NBUF) & 1);
-                if (ready) {
-                    tc_fence_after();
-                    const uint32_t a_lo = (uint32_t)de + ((buf * C::E_BYTES + s.p * 2 * C::SLICE) >> 4);
-                    const uint32_t b_lo = (uint32_t)dq + (s.p * 2 * C::QSLICE >> 4), d = tmem + kCols * sb;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {  // 16 channels each, 64 of a slice
-                        const uint32_t b_at = b_lo + (((kk >> 2) * C::QSLICE + (kk & 3) * 32) >> 4);
-                        if constexpr (C::THROUGH_TMEM)
-                            mma_tmem(d, tmem + C::TMEM_E + kCols * (s.p & 1) + 8 * kk, b_at, q_hi, IDESC_S, kk > 0 || s.p > 0);
-                        else
-                            mma(d, a_lo + (((kk >> 2) * C::SLICE + (kk & 3) * 32) >> 4), e_hi, b_at, q_hi, IDESC_S, kk > 0 || s.p > 0);
-                    }
-                    if constexpr (C::THROUGH_TMEM) mma_commit(smem_u32(&ms->a_free[s.p & 1]));
-                    if (++s.p == C::PARTS) {
-                        mma_commit(smem_u32(&ms->s_full[sb]));
-                        if (s.mine == 1) mma_commit(smem_u32(&ms->q_free));
-                        next_tile(s);
-                    }
-                    moved = true;
-                }
+            if (!ok) {
+                ms->abort = 1;
+                // nothing issued may still run when the CTA leaves
+                mma_commit(smem_u32(&ms->drain[scores]));
+                mbar_wait_for(smem_u32(&ms->drain[scores]), 0, kDrainCycles);
             }
-            if (moved) {
-                since = clock64();
-            } else if (*abort || clock64() - since > kWaitCycles) {
-                ok = false;
-                break;
-            }
-        }
-        if (!ok) {
-            ms->abort = 1;
-            // nothing issued may still run when the CTA leaves
-            mma_commit(smem_u32(&ms->drain));
-            mbar_wait_for(smem_u32(&ms->drain), 0, kDrainCycles);
         }
     }
     __syncwarp();
