@@ -8,7 +8,7 @@
 //   copy_check_kernel  (with long lists only) finds where each job's list ends: one
 //                      thread block per 4096 entries. Lists of together up to 32768
 //                      entries are read by the plan kernel, one warp a job, which
-//                      saves a launch (about 4 us of a small call's 18).
+//                      saves a launch (about 4 us of a small call).
 //   copy_plan_kernel   one thread block: counts, refusals, the flat list of
 //                      tiles (64 blocks each) and the new n_blocks.
 //   cache_move_kernel  four or more thread blocks per SM take tiles from a

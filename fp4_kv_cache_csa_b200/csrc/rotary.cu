@@ -12,7 +12,7 @@
 // relative, and it is reduced to [-pi, pi] in float64 with 2 pi in two parts
 // (an argument of 2^20 would lose all but four bits of its fraction in float32);
 // sine and cosine of the reduced angle, taken as a multiple of pi, are float32, and turned on by what that
-// multiple's rounding left (without it float32 outputs are 1.4 times as far from the exact ones).
+// multiple's rounding left (without it float32 outputs are 1.2 to 1.5 times as far from the exact ones).
 //
 // HBM-bound: each vector is read and written once (in place only its rotated
 // channels). A CTA takes a run of vectors (token, head), about four 8-channel
