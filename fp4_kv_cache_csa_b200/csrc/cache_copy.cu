@@ -3,7 +3,9 @@
 //
 // No arithmetic: every kept block's bytes of every plane (codes, scales, indexer
 // keys, their scales) are read once and written once per destination, so the
-// call is HBM-bound; small calls are bound by the latency of its launches.
+// call is HBM-bound: 2 x 262143 blocks of 400 bytes to two slots each take 109 us
+// (5.8 TB/s), 65521 listed blocks of 32 slots 318 us (5.3 TB/s). Small calls are
+// bound by the latency of its launches.
 //
 //   copy_check_kernel  (with long lists only) finds where each job's list ends: one
 //                      thread block per 4096 entries. Lists of together up to 32768

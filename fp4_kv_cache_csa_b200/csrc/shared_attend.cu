@@ -32,9 +32,10 @@
 // What bounds it: the chain S^T -> softmax -> O^T -> dequantization of the freed parts. Measured at D = 512, 64
 // heads: a tile of 64 columns takes about 5600 cycles, of which S^T's last part 420, the softmax to the last warp's
 // P' 1950 (512 of them exponentials, at 16 a cycle), O^T's first part 500 and the dequantization of two parts by
-// each team 2100 (1700 of them conversions, at 19 pairs a cycle), with a few hundred for each hand-over. An MMA of M = 128, N = 64, K = 16 takes 48 cycles here
+// each team 2100, with a few hundred for each hand-over. (The last is bound by issue rather than by the conversions:
+// integer instructions for a quarter of them took 1.47 ms.) An MMA of M = 128, N = 64, K = 16 takes 48 cycles here
 // (A's 4 KB from shared memory) against 32 at the tensor rate, so the products alone would take 3000.
-// 512 queries x 64 heads over 16384 blocks, causal: 1.43 ms, 0.77 PFLOP/s.
+// 512 queries x 64 heads over 16384 blocks, causal: 1.42 ms, 0.77 PFLOP/s.
 //
 // Three things that mattered more than the count of instructions. (1) The roles' loops share an instruction cache
 // that they overflow easily, and misses then go to one that all SMs of a GPC share: with E' of S^T passed through
