@@ -353,7 +353,11 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
         __syncthreads();
         if (in_place) {
             int *fl = a.flags + (size_t)lo * a.list_tiles;
+#ifdef CSA_TEST_LOST_ARRIVALS  // a test build in which the tiles that wait for a job's first one wait in vain
+            if (threadIdx.x == 0 && tile != 0) {
+#else
             if (threadIdx.x == 0) {
+#endif
                 __threadfence();
                 asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(fl + tile), "r"(1) : "memory");
             }

@@ -970,7 +970,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+#ifdef CSA_TEST_LOST_ARRIVALS  // a test build in which nothing completes the first wait for the queries
+                if (lane == 0 && warp != kSoftmaxWarps)
+#else
+                if (lane == 0)
+#endif
+                    mbar_arrive(smem_u32(&ms->q_full));
             }
             const int buf = n % C::NBUF, use = n / C::NBUF;
             if (D == 128 && (n & 1) != team) {
