@@ -556,7 +556,8 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
     rope = _CRope(inv_freq.data_ptr(), dim - rot if rot_begin is None else rot_begin, rot, layout, mscale)
 
     def call(s):
-        to = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+        # (empty_like takes a third of empty's time)
+        to = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format) if out is None else out
         co = cx if to is x else _vectors(what, "out", to)
         _check(lib.csa_rotary(ctypes.byref(cx), ctypes.byref(co), rows, heads, dim, ctypes.byref(rope), pos.data_ptr(),
                               int(inverse), s), what)
