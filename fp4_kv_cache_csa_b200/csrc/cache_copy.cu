@@ -3,8 +3,8 @@
 //
 // No arithmetic: every kept block's bytes of every plane (codes, scales, indexer
 // keys, their scales) are read once and written once per destination, so the
-// call is HBM-bound: 2 x 262143 blocks of 400 bytes to two slots each take 109 us
-// (5.8 TB/s), 65521 listed blocks of 32 slots 318 us (5.3 TB/s). Small calls are
+// call is HBM-bound: 2 x 262143 blocks of 400 bytes to two slots each take 107 us
+// (5.9 TB/s), 65521 listed blocks of 32 slots 298 us (5.65 TB/s). Small calls are
 // bound by the latency of its launches.
 //
 //   copy_check_kernel  (with long lists only) finds where each job's list ends: one
@@ -25,8 +25,9 @@
 // later ones). Every tile loads all its rows before it writes, and sets a flag in
 // between; a tile writes once the tiles whose sources lie in its destination have
 // set theirs -- as a rule one or two, found by searching the list while the rows
-// load. Tiles are handed out in order and loading waits for nothing, so a tile
-// only ever waits for tiles that running thread blocks hold.
+// load. Tiles are handed out in order, each thread block one ahead, and
+// loading waits for nothing: of the tiles that have not loaded the first one is never
+// behind a tile that still waits, so every wait ends.
 #include "common.cuh"
 #include "tc_util.cuh"
 
@@ -265,7 +266,8 @@ __device__ __forceinline__ void copy_out(uint8_t *to, const uint8_t *from, uint3
 }
 
 // First position in the ascending list[0, n) whose entry is >= v, by one warp: 32 probes a step.
-__device__ __forceinline__ int lower_bound_warp(const int32_t *list, int n, int v) {
+template <typename T>
+__device__ __forceinline__ int lower_bound_warp(const T *list, int n, T v) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = n;  // the answer lies in [lo, hi]
     while (lo < hi) {
@@ -283,38 +285,48 @@ __device__ __forceinline__ int lower_bound_warp(const int32_t *list, int n, int 
 
 __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
     extern __shared__ __align__(16) uint8_t buf[];
-    __shared__ int s_idx[kTileRows];
+    __shared__ int s_idx[2][kTileRows];
     __shared__ long long s_ticket;
     __shared__ int s_dep[2];
     __shared__ int s_late;
     grid_dep_wait();
     const long long total = a.prefix[a.jobs];
     const int warp = threadIdx.x >> 5;
+    struct Tile {
+        int job, tile;
+        JobRec r;
+    };
+    // Where tile t lies, and its list entries on their way to `idx`. The next tile's are found while the rows of this
+    // one load: five dependent loads or more that every tile used to begin with (318 us for the 32 slots above).
+    auto find = [&](long long t, int *idx) {
+        Tile x = {};
+        if (t < total) {
+            x.job = lower_bound_warp(a.prefix + 1, a.jobs - 1, t + 1);  // prefix[job] <= t < prefix[job + 1]
+            x.r = a.rec[x.job];
+            x.tile = (int)(t - a.prefix[x.job]);
+            const int k = x.tile * kTileRows + threadIdx.x;
+            if (a.keep && threadIdx.x < kTileRows && k < x.r.n) idx[threadIdx.x] = __ldg(a.keep + (size_t)x.job * a.cols + k);
+        }
+        return x;
+    };
     if (threadIdx.x == 0) s_ticket = (long long)atomicAdd(a.ticket, 1ull);
     __syncthreads();
-    long long t = s_ticket;
-    while (t < total) {
-        // the job that holds tile t: prefix[j] <= t < prefix[j + 1]
-        int lo = 0, hi = a.jobs - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.prefix[mid + 1] <= t) lo = mid + 1; else hi = mid;
-        }
-        const JobRec r = a.rec[lo];
-        const int tile = (int)(t - a.prefix[lo]);
-        const int j0 = tile * kTileRows, rows = min(kTileRows, r.n - j0);
+    long long t = s_ticket, t_next;
+    Tile now = find(t, s_idx[0]), next;
+    for (int cur = 0; t < total; t = t_next, now = next, cur ^= 1) {
+        const JobRec r = now.r;
+        const int lo = now.job, tile = now.tile, j0 = tile * kTileRows, rows = min(kTileRows, r.n - j0);
         const int32_t *list = a.keep ? a.keep + (size_t)lo * a.cols : nullptr;
         const bool in_place = a.same && r.src == r.dst;
-        __syncthreads();  // everyone has read s_ticket, and has left the shared buffers of the tile before
-        if (list && threadIdx.x < rows) s_idx[threadIdx.x] = __ldg(list + j0 + threadIdx.x);
+        const int *idx = s_idx[cur];
+        __syncthreads();  // the indices are there; everyone has read s_ticket and left the buffers of the tile before
         if (threadIdx.x == 0) {
             s_ticket = (long long)atomicAdd(a.ticket, 1ull);
             s_late = 0;
         }
-        __syncthreads();
         const uint32_t buf_s = smem_u32(buf);
         // an in-place tile whose blocks stay where they are: ascending, so the two ends tell
-        const bool still = in_place && s_idx[0] == j0 && s_idx[rows - 1] == j0 + rows - 1;
+        const bool still = in_place && idx[0] == j0 && idx[rows - 1] == j0 + rows - 1;
         uint32_t at[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -335,12 +347,12 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
 #pragma unroll 4
                     for (uint32_t k = threadIdx.x; k < n; k += kMoveThreads) {
                         const uint32_t row = k >> shift, o = (k & (per - 1)) * 16;
-                        copy_in_unit(buf_s + at[q] + k * 16, src + (size_t)s_idx[row] * pl.row + o, 16);
+                        copy_in_unit(buf_s + at[q] + k * 16, src + (size_t)idx[row] * pl.row + o, 16);
                     }
                 } else {
                     for (uint32_t k = threadIdx.x; k < n; k += kMoveThreads) {
                         const uint32_t row = k / per, o = (k - row * per) * unit;
-                        copy_in_unit(buf_s + at[q] + row * pl.row + o, src + (size_t)s_idx[row] * pl.row + o, unit);
+                        copy_in_unit(buf_s + at[q] + row * pl.row + o, src + (size_t)idx[row] * pl.row + o, unit);
                     }
                 }
             }
@@ -349,6 +361,9 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
             const int p = lower_bound_warp(list, min(r.n, j0 + rows), warp == 0 ? j0 : j0 + rows);
             if ((threadIdx.x & 31) == 0) s_dep[warp] = p;
         }
+        __syncthreads();  // s_ticket
+        t_next = s_ticket;
+        next = find(t_next, s_idx[cur ^ 1]);
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         if (in_place) {
@@ -378,7 +393,6 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
             __syncthreads();
             if (s_late) {  // never written over blocks that were not read: the slot's tail is invalid
                 if (threadIdx.x == 0) flag(a.status, CSA_DEV_TIMEOUT);
-                t = s_ticket;
                 continue;
             }
         }
@@ -393,7 +407,6 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
                 }
             }
         }
-        t = s_ticket;
     }
 }
 
