@@ -180,6 +180,22 @@ def test_splits(D, H, P, Nq, n):
     run(random_cache(P, n, D, n=[n - 13 * p for p in range(P)]), [0, *w.tolist(), Nq], H, join=Nq % 2 == 0)
 
 
+@pytest.mark.parametrize("D,H,Nq,n,causal", [(128, 64, 1301, 300, False), (512, 33, 700, 517, True)])
+def test_more_groups_than_the_small_plan_takes(D, H, Nq, n, causal):
+    c = random_cache(3, n, D, n=[n, 0, n - 130])
+    pos = np.random.default_rng(1).integers(-2, 4 * n + 8, Nq) if causal else None
+    run(c, [0, Nq // 2, Nq // 2 + 7, Nq], H, pos=pos, join=causal)
+
+
+def test_more_slots_than_the_small_plan_takes():
+    rng = np.random.default_rng(2)
+    P = 1100
+    n = rng.integers(0, 140, P)
+    queries = rng.integers(0, 3, P)
+    queries[[0, -1]] = 0
+    run(random_cache(P, 139, 128, n=n.tolist()), [0, *np.cumsum(queries).tolist()], 16, join=True)
+
+
 def test_against_the_oracle_and_hca_decode_attend():
     import torch
 
