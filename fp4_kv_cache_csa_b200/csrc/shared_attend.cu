@@ -19,9 +19,13 @@
 // blocks, N = 64 columns), O^T += E'^T P' (M = 128 channels, N = 64, K = 128 blocks).
 // Operands are fp16: E'_j = e_j 2^-R_j and q' = q 2^-sQ are exact (R_j: the row's
 // largest E8M0 exponent, 7 with E4M3 scales; sQ puts each column's max |q| into
-// [2^14, 2^15)); P' = 2^(u log2 e + (R_j - B) - rho) <= 2^8, with B a common exponent, is
+// [2^14, 2^15)); P' = 2^(u log2 e + (R_j - B) - rho) <= 2^15, with B a common exponent, is
 // rounded to fp16's 11 bits, which leaves about 1e-4 of the output's norm, an order
-// below the bf16 rounding of the output. Row sums, references and accumulators are float32.
+// below the bf16 rounding of the output. References rho lie 7 bits below the largest logit that
+// they were taken from, so that a weight loses bits only below 2^-21 of the largest one, and all of them
+// below 2^-32: what n such blocks are short of together is n 2^-32 of the output (2^-13 at 2^19 blocks; with
+// references at the largest logit it was 2^-25 a block, 0.8% at 2^18). Row sums, references and accumulators are
+// float32.
 //
 // Warp roles (20 warps, one CTA per SM): eight dequantize (they also bring the group's queries in), eight do the
 // softmax and the outputs, two prepare the rows' exponents and scale factors a tile ahead, one thread each issues
@@ -73,6 +77,9 @@ constexpr int kExponentSpan = 40, kEvenBelow = 10, kEvenAbove = 12;
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
+// P' in bits: what a column's largest logit starts at when its reference is taken, and from where on the reference is
+// raised. Eight bits between them make a raise rare; fp16 ends at 2^16.
+constexpr float kStartBits = 7.f, kMostBits = 15.f;
 // Calls of up to so many groups and slots are planned in shared memory (2.5 instead of 5.6 us; planned by every CTA of
 // the main kernel for itself, a launch less, they made that kernel's registers spill: 94 -> 106 us at 32 queries then).
 constexpr int kSmallGroups = 512;
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 tc_fence_after();
                 float u[32];
                 // u + R - rho of this thread's rows and columns. References are set by the group's first tile, and
-                // raised (with O^T and the sums) when a logit exceeds one by more than 8: then once more from
+                // raised (with O^T and the sums) when a logit exceeds one by more than kMostBits: then once more from
                 // the start, with the new ones. (A second raise happens only where a logit is so large that
                 // the first one was rounded; what rounding then leaves above is cut.) A wait that ran out
                 // comes this way too.
@@ -690,12 +697,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     }
                     if (pass >= 2) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) u[k] = u[k] > 8.f ? 8.f : u[k];
+                        for (int k = 0; k < 32; ++k) u[k] = u[k] > kMostBits ? kMostBits : u[k];
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) over = fmaxf(over, fmaxf(fmaxf(u[k], u[k + 8]), fmaxf(u[k + 16], u[k + 24])));
                     const bool set = first && pass == 0;
-                    if (!bar_or_n<kSoftmaxThreads>(set || over > 8.f || !ok)) break;
+                    if (!bar_or_n<kSoftmaxThreads>(set || over > kMostBits || !ok)) break;
                     if (!first) ok = ok && wait(&ms->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort);
                     float2 m[8];
 #pragma unroll
@@ -713,9 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
 #pragma unroll
                         for (int w = 1; w < kSoftmaxWarps; ++w) M = fmaxf(M, ms->wred[w][tid]);
                         // (a column that sees nothing of its first tile sees nothing of the others)
-                        const bool raise = set ? M > -INFINITY : M > 8.f;
-                        if (raise) ms->minus_rho[tid] -= M;
-                        ms->alpha[tid] = raise ? pow2(-M) : 1.f;
+                        const bool raise = set ? M > -INFINITY : M > kMostBits;
+                        if (raise) ms->minus_rho[tid] -= M - kStartBits;
+                        ms->alpha[tid] = raise ? pow2(kStartBits - M) : 1.f;
                     }
                     bar_sync_n<kSoftmaxThreads>();
                     if (!first) {
