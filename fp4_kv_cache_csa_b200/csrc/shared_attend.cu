@@ -68,12 +68,15 @@ constexpr int kTeamWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;  // S^T; the one behind it: O^T
 constexpr int kFactorWarp = kMmaWarp + 2, kFactorWarps = 2;
 // Row exponents count from B, the largest of the group's first tile in the CTA (127, that is 1, when
-// its rows are all zero). fp16 holds a row of 2^(B - 10) .. 2^(B + 12) exactly without an exponent of its own
-// (groups down to 2^-13 of the row's largest, which a row at B has down to 2^-23), and then takes none: R = 0. Others
-// take theirs, but at least B - 40: what that flushes to zero lies below 2^-64 of the first tile's scale,
-// and no sum leaves float32's range over all-zero rows (scale byte 0).
+// its rows are all zero), or kLeastBase if that is larger. fp16 holds a row of 2^(B - 10) .. 2^(B + 12) exactly without
+// an exponent of its own (groups down to 2^-13 of the row's largest, which a row at B has down to 2^-23), and then
+// takes none: R = 0. Others take theirs, but at least B - kExponentSpan: what that flushes to zero lies below 2^-104 of
+// the first tile's scale (none where B is kLeastBase, whose rows reach down to byte 1), and no sum leaves float32's
+// range over all-zero rows (scale byte 0; 2^(15 + 80) each). With kLeastBase, factors 2^(R - B) stay in float32's
+// range for rows up to byte 207 (2^80) behind a first tile of any scale; counted from the tile's own B, ordinary rows
+// behind a tile of scale byte 1 gave NaN.
 constexpr int kNoRow = 1024;  // of a row behind the last visible one: its factors come out 0
-constexpr int kExponentSpan = 40, kEvenBelow = 10, kEvenAbove = 12;
+constexpr int kExponentSpan = 80, kLeastBase = kExponentSpan + 1, kEvenBelow = 10, kEvenAbove = 12;
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)
 constexpr long long kTileUnits = 100, kStartUnits = 150;
 constexpr int kScaleE8M0x32 = 0, kScaleE4M3x16 = 1;
@@ -499,7 +502,7 @@ __device__ __forceinline__ void reduce_columns(float2 (&v)[8]) {
 // B + 127 from what the factor warps found (E8M0).
 __device__ __forceinline__ int base_of(const int (&b)[kFactorWarps]) {
     const int m = max(b[0], b[1]);
-    return m > 0 ? m : 127;
+    return m > 0 ? max(m, kLeastBase) : 127;
 }
 
 // lse of a column, and the factor of its accumulator, from its reference and row sum; joined with
@@ -843,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                         for (int e = 0; e < 2; ++e) {
                             const int col = col0 + k + e;
                             const float f = ms->fac[col];
-                            v[e] = f == 0.f ? 0.f : o[k + e] * (f * unit);  // (a NaN goes on)
+                            v[e] = f == 0.f ? 0.f : o[k + e] * f * unit;  // (a NaN goes on; f * unit alone may lie below float32's range)
                             if (a.join_lse && col < cols && ms->jfac[col] != 0.f)
                                 v[e] = fmaf(ms->jfac[col], jo[(size_t)(k + e) * D], v[e]);
                         }
