@@ -23,6 +23,8 @@
 // (both in one CTA: 210 us for 8192 x 64 x 512 bf16, apart: 175 us).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace csa {
@@ -129,6 +131,25 @@ __device__ __forceinline__ void store(T *p, const float (&v)[CH], bool wide) {
     }
 }
 
+// The words of channels that keep their type, as they are (a conversion would rewrite the payloads of NaNs).
+template <typename T, int CH>
+__device__ __forceinline__ void store_words(T *p, const Words<T, CH> &r, bool wide) {
+    if (CH * sizeof(T) == 32 && wide) {
+        if constexpr (CH * sizeof(T) == 32)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]),
+                         "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                         : "memory");
+    } else if constexpr (CH * sizeof(T) >= 16) {
+#pragma unroll
+        for (int k = 0; k < (int)(CH * sizeof(T)) / 16; ++k)
+            reinterpret_cast<uint4 *>(p)[k] = make_uint4(r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint32_t *>(p) = r.w[0];
+    } else {
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)r.w[0];
+    }
+}
+
 // pos * f reduced to [-pi, pi], then (cos, sin) * mscale
 __device__ __forceinline__ float2 angle(int pos, float f, float mscale, float sign) {
     constexpr double kPi = 3.14159265358979311600, kInvPi = 0.31830988618379067154;
@@ -199,9 +220,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
             if (u_first + threadIdx.x + i * kThreads >= total) break;
-            float v[CH];
-            unpack<TI, CH>(w[i], v);
-            store<TO, CH>(out + to[i], v, a.wide_out);
+            if constexpr (std::is_same<TI, TO>::value) {
+                store_words<TO, CH>(out + to[i], w[i], a.wide_out);
+            } else {
+                float v[CH];
+                unpack<TI, CH>(w[i], v);
+                store<TO, CH>(out + to[i], v, a.wide_out);
+            }
         }
         return;
     }

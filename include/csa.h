@@ -429,7 +429,8 @@ csa_status csa_cache_copy(const csa_cache *src, const csa_cache *dst, int32_t n_
  * Rotary positions. Vector (row i, head h) is `dim` channels at
  * data + i * row_stride + h * head_stride (strides in elements); the channels
  * [rot_begin, rot_begin + rot_dim) are turned pairwise by angles that grow with
- * the row's token position, the others are copied:
+ * the row's token position, the others are copied (bit for bit where out has x's
+ * type, else rounded once):
  *   t = pos[i] * inv_freq[p],  0 <= p < rot_dim / 2
  *   y_a = mscale * (a cos t - b sin t),  y_b = mscale * (a sin t + b cos t)
  * with (a, b) the channels rot_begin + (2p, 2p + 1) (CSA_ROPE_PAIRS) or
