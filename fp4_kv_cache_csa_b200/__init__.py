@@ -540,7 +540,8 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
     """Rotary positions: x [rows, (heads,) dim] bf16 or float32 (any strides, channels adjacent) with the
     channels [rot_begin, rot_begin + 2 len(inv_freq)) turned by pos [rows] int32 * inv_freq float32
     (rot_begin: the last ones by default). Returns `out`: x itself turns it in place; by default a new
-    tensor of out_dtype (x's type). inverse=True turns back, and is the gradient."""
+    tensor of out_dtype (x's type). inverse=True turns back, and is the gradient of x: the backward pass of a
+    caller's autograd function. The call itself records none, and refuses tensors that require one."""
     import torch
 
     lib, what = load_library(), "csa_rotary"
@@ -550,6 +551,10 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
     if out is not None and (out.shape != x.shape or out.device != x.device or
                             (out_dtype is not None and out.dtype != out_dtype)):
         raise CsaError(f"{what}: out must match x's shape and device, and out_dtype")
+    if torch.is_grad_enabled() and (x.requires_grad or inv_freq.requires_grad or
+                                    (out is not None and out.requires_grad)):
+        raise CsaError(f"{what} records no gradient: call it on detached tensors or under torch.no_grad(); the "
+                       "gradient of x is csa_rotary(dy, ..., inverse=True)")
     rot = 2 * inv_freq.shape[0] if inv_freq.dim() else 0
     _expect(what, "pos", pos, x.device, torch.int32, (rows,))
     _expect(what, "inv_freq", inv_freq, x.device, torch.float32, (rot // 2,))
@@ -561,6 +566,8 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
         co = cx if to is x else _vectors(what, "out", to)
         _check(lib.csa_rotary(ctypes.byref(cx), ctypes.byref(co), rows, heads, dim, ctypes.byref(rope), pos.data_ptr(),
                               int(inverse), s), what)
+        if out is not None:
+            torch.autograd.graph.increment_version(out)  # who kept it for a backward pass finds it changed
         return to
 
     return _on(x.device, stream, call)
