@@ -449,7 +449,8 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
     """Dense attention of many queries over one slot's blocks (a prompt that continuations share, a prefill
     chunk), each tile dequantized once for 64 (query, head) columns; joined with (join_out, join_lse), the
     float32 result of a query's own part, as one softmax. Without q_pos every query sees all blocks of its
-    slot. q [Nq, H, D] bf16; returns out [Nq, H, D] bf16, and fills lse [Nq, H] float32 if given."""
+    slot. q [Nq, H, D] bf16; returns out [Nq, H, D] bf16, and fills lse [Nq, H] float32 if given. No gradient
+    is recorded."""
     import torch
 
     lib, what = load_library(), "hca_shared_attend"
@@ -480,6 +481,9 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
         _check(lib.hca_shared_attend(c, q.data_ptr(), n, heads, q_offsets.data_ptr(), _ptr(q_pos), _ptr(join_out),
                                      _ptr(join_lse), D ** -0.5 if softmax_scale is None else softmax_scale,
                                      to.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, s), what)
+        for t in (out, lse):
+            if t is not None:
+                torch.autograd.graph.increment_version(t)  # as in csa_rotary
         return to
 
     return _on(device, stream, call)
