@@ -770,7 +770,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[n % C::NP]));
+#ifdef CSA_TEST_LOST_WEIGHTS  // a test build in which O^T waits in vain for the last tile's weights
+                if (lane == 0 && !(warp == 0 && c.left == 1))
+#else
+                if (lane == 0)
+#endif
+                    mbar_arrive(smem_u32(&ms->p_full[n % C::NP]));
                 // the sums (without 2^R, which P' carries for E'), while the O^T product runs
                 if (even) {
 #pragma unroll
@@ -1199,12 +1204,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                     next_tile(n);
                 }
             }
-            if (!ok) {
-                ms->abort = 1;
-                // nothing issued may still run when the CTA leaves
-                mma_commit(smem_u32(&ms->drain[scores]));
-                mbar_wait_for(smem_u32(&ms->drain[scores]), 0, kDrainCycles);
-            }
+            // Nothing issued may still run when the CTA leaves, and others may give up after this thread's last product
+            // has gone out. (Otherwise they wait for it themselves: this costs nothing.)
+            mma_commit(smem_u32(&ms->drain[scores]));
+            if (!mbar_wait_for(smem_u32(&ms->drain[scores]), 0, kDrainCycles) || !ok) ms->abort = 1;
         }
     }
     __syncwarp();
