@@ -43,6 +43,11 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanSmemBatch = 1024;
 constexpr int kPlanEntries = 32768;  // list entries that the plan kernel reads itself
 
+// Shared memory of a plane's tile: its rows, and room for the tile's offset from a 16-byte boundary.
+constexpr int tile_bytes(int row) { return (kTileRows * row + 15) / 16 * 16 + 16; }
+// The largest tile of any admitted layout: dim 512, E4M3 scales, bf16 keys of 256 channels.
+constexpr int kMostTileBytes = tile_bytes(256) + tile_bytes(32) + tile_bytes(512);
+
 struct Plane {
     const uint8_t *src;
     uint8_t *dst;
@@ -448,7 +453,7 @@ cudaError_t launch_cache_copy(const csa_cache &src, const csa_cache &dst, int jo
     int at = 0;
     auto plane = [&](const void *from, void *to, int row) {
         a.plane[a.planes++] = {static_cast<const uint8_t *>(from), static_cast<uint8_t *>(to), row, at};
-        at += (kTileRows * row + 15) / 16 * 16 + 16;  // room for the tile's offset from a 16-byte boundary
+        at += tile_bytes(row);
     };
     plane(src.fp4, dst.fp4, src.dim / 2);
     plane(src.scale, dst.scale, src.dim / (src.scale_fmt == CSA_SCALE_E4M3_16 ? 16 : 32));
@@ -481,7 +486,10 @@ cudaError_t launch_cache_copy(const csa_cache &src, const csa_cache &dst, int jo
     a.slot_tab = reinterpret_cast<int *>(base + l.slot_tab);
     a.part_end = reinterpret_cast<int *>(base + l.part_end);
     a.flags = reinterpret_cast<int *>(base + l.flags);
-    cudaError_t err;
+    // One limit for every layout: it belongs to the kernel, and threads that set their own call's could lower it between
+    // another's setting and its launch. Before the plan, which already writes n_blocks.
+    cudaError_t err = cudaFuncSetAttribute(cache_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostTileBytes);
+    if (err != cudaSuccess) return err;
     if (keep && !a.plan_lists) {
         copy_check_kernel<<<dim3(l.parts, jobs), 256, 0, s>>>(a);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
@@ -490,8 +498,6 @@ cudaError_t launch_cache_copy(const csa_cache &src, const csa_cache &dst, int jo
         copy_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    if ((err = cudaFuncSetAttribute(cache_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, at)) != cudaSuccess)
-        return err;
     // as many thread blocks as fit an SM's shared memory, up to its 2048 threads; no more than there can be tiles
     const long long most = (long long)jobs * (((long long)(keep ? min(cols, dst.capacity) : dst.capacity) + kTileRows - 1) / kTileRows);
     const long long grid = min(most, (long long)num_sms * max(1, min(8, 220 * 1024 / (at + 2048))));
