@@ -396,8 +396,13 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(CopyArgs a) {
                 }
             }
             __syncthreads();
-            if (s_late) {  // never written over blocks that were not read: the slot's tail is invalid
-                if (threadIdx.x == 0) flag(a.status, CSA_DEV_TIMEOUT);
+            // Never written over blocks that were not read. The slot then ends before the first such tile (later ones
+            // may be written), so that no old block counts as a kept one, with a status word or without.
+            if (s_late) {
+                if (threadIdx.x == 0) {
+                    atomicMin(a.dst_n + r.dst, j0);
+                    flag(a.status, CSA_DEV_TIMEOUT);
+                }
                 continue;
             }
         }

@@ -418,7 +418,9 @@ csa_status hca_shared_attend(const csa_cache *cache, const void *q, int32_t n_qu
  * would break that -- a slot written by a job before it, or, within one cache, a
  * slot that another job reads (unless the job only cuts it) -- is skipped and sets
  * CSA_DEV_BAD_INDEX in dst->status, as does a job with a slot out of range; one
- * that does not fit dst's capacity is skipped with CSA_DEV_CAPACITY.
+ * that does not fit dst's capacity is skipped with CSA_DEV_CAPACITY. Should a wait of
+ * an in-place compaction run out (CSA_DEV_TIMEOUT; it takes about a second, and
+ * a fault of the device), n_blocks ends before the first block that was not written.
  */
 size_t csa_cache_copy_workspace(const csa_cache *dst, int32_t n_jobs, int32_t keep_cols);
 csa_status csa_cache_copy(const csa_cache *src, const csa_cache *dst, int32_t n_jobs, const int32_t *src_slot,
