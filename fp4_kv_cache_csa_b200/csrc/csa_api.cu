@@ -443,7 +443,8 @@ csa_status csa_cache_copy(const csa_cache *src, const csa_cache *dst, int32_t n_
     csa_status st = check_cache(src);
     if (st != CSA_OK) return st;
     if ((st = check_cache(dst)) != CSA_OK) return st;
-    if (n_jobs < 0 || keep_cols < 0 || (keep == nullptr) != (keep_cols == 0)) return CSA_ERR_SHAPE;
+    if (n_jobs < 0 || keep_cols < 0) return CSA_ERR_SHAPE;
+    if (n_jobs > 0 && (keep == nullptr) != (keep_cols == 0)) return CSA_ERR_SHAPE;  // (no jobs: a list without an address)
     if (src->dim != dst->dim || src->block != dst->block || src->scale_fmt != dst->scale_fmt ||
         (src->idx_key == nullptr) != (dst->idx_key == nullptr))
         return CSA_ERR_SHAPE;

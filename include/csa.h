@@ -409,7 +409,8 @@ csa_status hca_shared_attend(const csa_cache *cache, const void *q, int32_t n_qu
  *              no memory, with the same dim, block and formats; batch and capacity
  *              may differ. dim at most 512.
  *   src_slot, dst_slot int32 [n_jobs] device; max_blocks int32 [n_jobs] device or NULL
- *   keep       int32 [n_jobs][keep_cols] device or NULL (then keep_cols is 0)
+ *   keep       int32 [n_jobs][keep_cols] device or NULL (then keep_cols is 0; with no
+ *              jobs it may be anything)
  *   n_jobs     0 (nothing is launched) .. 65535
  *   workspace  >= csa_cache_copy_workspace(dst, n_jobs, keep_cols) bytes, 256-byte aligned
  * Within one cache src_slot[i] == dst_slot[i] works in place: without a list it only
