@@ -8,9 +8,10 @@
 // bound by the latency of its launches.
 //
 //   copy_check_kernel  (with long lists only) finds where each job's list ends: one
-//                      thread block per 4096 entries. Lists of together up to 32768
-//                      entries are read by the plan kernel, one warp a job, which
-//                      saves a launch (about 4 us of a small call).
+//                      thread block per 4096 entries. Lists of up to 4096 columns
+//                      and together up to 32768 entries are read by the plan kernel,
+//                      one warp a job, which saves a launch (about 4 us of a small
+//                      call); a list is then one part, whose end that warp finds.
 //   copy_plan_kernel   one thread block: counts, refusals, the flat list of
 //                      tiles (64 blocks each) and the new n_blocks.
 //   cache_move_kernel  four or more thread blocks per SM take tiles from a
@@ -41,7 +42,7 @@ constexpr int kFan = 4;          // destinations that share the read of a tile
 constexpr int kCheckPart = 4096; // list entries of one check block
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSmemBatch = 1024;
-constexpr int kPlanEntries = 32768;  // list entries that the plan kernel reads itself
+constexpr int kPlanEntries = 32768;  // list entries that the plan kernel reads itself, in lists of one part
 
 // Shared memory of a plane's tile: its rows, and room for the tile's offset from a 16-byte boundary.
 constexpr int tile_bytes(int row) { return (kTileRows * row + 15) / 16 * 16 + 16; }
@@ -483,7 +484,7 @@ cudaError_t launch_cache_copy(const csa_cache &src, const csa_cache &dst, int jo
     a.jobs = jobs;
     a.cols = cols;
     a.plan_lists = keep && cols <= kCheckPart && (long long)jobs * cols <= kPlanEntries;
-    a.parts = l.parts;  // (1 where the plan kernel reads the lists)
+    a.parts = l.parts;  // (1 where the plan kernel reads the lists: it writes no other part's end)
     a.list_tiles = l.list_tiles;
     a.rec = reinterpret_cast<JobRec *>(base + l.rec);
     a.prefix = reinterpret_cast<long long *>(base + l.prefix);
