@@ -127,7 +127,9 @@ typedef struct {
 const char *csa_status_string(int32_t status);
 
 /* Library ABI version (major * 100 + minor). 101 added csa_cache.scale_fmt, 102 the pool and
- * Reindex calls, 103 the MXFP4 indexer keys (csa_cache.idx_key_scale). */
+ * Reindex calls, 103 the MXFP4 indexer keys (csa_cache.idx_key_scale). hca_shared_attend,
+ * csa_cache_copy, csa_rotary and csa_rotary_frequencies came without a new number: they change
+ * no structure or call of 103, and a library that has them is told by their symbols. */
 int32_t csa_version(void);
 
 /*
