@@ -186,11 +186,22 @@ def _raw_stream(index):
     return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _expect(what, name, t, device, dtype, shape):
-    """One tensor of a call: on `device`, of `dtype`, dense, of this shape."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise CsaError(f"{what}: {name} must be a dense {dtype} tensor {list(shape)} on {device}, not "
-                       f"{t.dtype} {list(t.shape)}{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
+def _expect(what, name, t, at, dtype, shape):
+    """One tensor of a call: on device number `at` (-1: the host), of `dtype`, dense, of this shape."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != at or not t.is_contiguous():
+        raise CsaError(f"{what}: {name} must be a dense {dtype} tensor {list(shape)} on {f'cuda:{at}' if at >= 0 else 'cpu'}, "
+                       f"not {t.dtype} {list(t.shape)}{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
+
+
+def _expect_cache(what, c, at, int32):
+    """A cache of a call whose tensors are on device number `at`: dense planes whose sizes belong together, and int32
+    counts beside them (with others a kernel would read and write elsewhere)."""
+    n, fp4, scale, key = c.n_blocks, c.fp4, c.scale, c.idx_key
+    if (fp4.get_device() != at or n.get_device() != at or n.dtype is not int32 or n.numel() != fp4.shape[0]
+            or scale.numel() * (16 if c.scale_fmt == CSA_SCALE_E8M0_32 else 8) != fp4.numel()  # (codes: two a byte)
+            or not fp4.is_contiguous() or not scale.is_contiguous() or (key is not None and not key.is_contiguous())):
+        raise CsaError(f"{what}: a cache's planes must be dense tensors [batch, capacity, row] on the call's device, with "
+                       "rows of its scale format, and n_blocks int32 [batch]")
 
 
 def _expect_workspace(what, ws, device):
@@ -237,9 +248,11 @@ class Cache:
 
     def c_struct(self) -> _CCache:
         batch, capacity, half = self.fp4.shape
+        key, key_scale, status = self.idx_key, self.idx_key_scale, self.status
         return _CCache(batch, 2 * half, self.block, capacity, self.fp4.data_ptr(), _ptr(self.scale),
-                       _ptr(self.idx_key), self.idx_dim, self.idx_dtype, _ptr(self.n_blocks), _ptr(self.status),
-                       self.scale_fmt, _ptr(self.idx_key_scale))
+                       None if key is None else key.data_ptr(), 0 if key is None else self.idx_dim, self.idx_dtype,
+                       _ptr(self.n_blocks), None if status is None else status.data_ptr(), self.scale_fmt,
+                       None if key_scale is None else key_scale.data_ptr())
 
     @staticmethod
     def allocate(batch: int, capacity: int, dim: int, block: int, idx_dim: int = 0, idx_dtype: int = CSA_IDX_BF16,
@@ -458,20 +471,20 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
     if q.dim() != 3:
         raise CsaError(f"{what}: q must be [queries, heads, dim], not {list(q.shape)}")
     n, heads, D = q.shape
-    _expect(what, "q", q, device, torch.bfloat16, (n, heads, cache.dim))
-    if cache.fp4.device != device:
-        raise CsaError(f"{what}: cache is on {cache.fp4.device}, q on {device}")
-    _expect(what, "q_offsets", q_offsets, device, i32, (cache.batch + 1,))
+    at = q.get_device()
+    _expect(what, "q", q, at, torch.bfloat16, (n, heads, cache.dim))
+    _expect_cache(what, cache, at, i32)
+    _expect(what, "q_offsets", q_offsets, at, i32, (cache.batch + 1,))
     if q_pos is not None:
-        _expect(what, "q_pos", q_pos, device, i32, (n,))
+        _expect(what, "q_pos", q_pos, at, i32, (n,))
     if join_out is not None:
-        _expect(what, "join_out", join_out, device, f32, (n, heads, D))
+        _expect(what, "join_out", join_out, at, f32, (n, heads, D))
     if join_lse is not None:
-        _expect(what, "join_lse", join_lse, device, f32, (n, heads))
+        _expect(what, "join_lse", join_lse, at, f32, (n, heads))
     if out is not None:
-        _expect(what, "out", out, device, torch.bfloat16, (n, heads, D))
+        _expect(what, "out", out, at, torch.bfloat16, (n, heads, D))
     if lse is not None:
-        _expect(what, "lse", lse, device, f32, (n, heads))
+        _expect(what, "lse", lse, at, f32, (n, heads))
     _expect_workspace(what, workspace, device)
     c = ctypes.byref(cache.c_struct())
 
@@ -503,18 +516,20 @@ def csa_cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, keep=None, max_bl
 
     lib, what = load_library(), "csa_cache_copy"
     device, n, i32 = src.fp4.device, src_slot.shape[0] if src_slot.dim() else -1, torch.int32
-    if dst.fp4.device != device:
-        raise CsaError(f"{what}: src is on {device}, dst on {dst.fp4.device}")
-    _expect(what, "src_slot", src_slot, device, i32, (n,))
-    _expect(what, "dst_slot", dst_slot, device, i32, (n,))
+    at = src.fp4.get_device()
+    _expect_cache(what, src, at, i32)
+    if dst is not src:
+        _expect_cache(what, dst, at, i32)
+    _expect(what, "src_slot", src_slot, at, i32, (n,))
+    _expect(what, "dst_slot", dst_slot, at, i32, (n,))
     cols = 0
     if keep is not None:
         cols = keep.shape[-1] if keep.dim() else 0
-        _expect(what, "keep", keep, device, i32, (n, cols))
+        _expect(what, "keep", keep, at, i32, (n, cols))
         if cols == 0:
             raise CsaError(f"{what}: keep needs a column (-1 in it keeps nothing)")
     if max_blocks is not None:
-        _expect(what, "max_blocks", max_blocks, device, i32, (n,))
+        _expect(what, "max_blocks", max_blocks, at, i32, (n,))
     _expect_workspace(what, workspace, device)
     cs = src.c_struct()
     cd = cs if dst is src else dst.c_struct()
@@ -560,8 +575,9 @@ def csa_rotary(x, pos, inv_freq, out=None, rot_begin: Optional[int] = None, layo
         raise CsaError(f"{what} records no gradient: call it on detached tensors or under torch.no_grad(); the "
                        "gradient of x is csa_rotary(dy, ..., inverse=True)")
     rot = 2 * inv_freq.shape[0] if inv_freq.dim() else 0
-    _expect(what, "pos", pos, x.device, torch.int32, (rows,))
-    _expect(what, "inv_freq", inv_freq, x.device, torch.float32, (rot // 2,))
+    at = x.get_device()
+    _expect(what, "pos", pos, at, torch.int32, (rows,))
+    _expect(what, "inv_freq", inv_freq, at, torch.float32, (rot // 2,))
     rope = _CRope(inv_freq.data_ptr(), dim - rot if rot_begin is None else rot_begin, rot, layout, mscale)
 
     def call(s):
