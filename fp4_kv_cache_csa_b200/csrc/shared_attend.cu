@@ -73,8 +73,9 @@ constexpr int kFactorWarp = kMmaWarp + 2, kFactorWarps = 2;
 // takes none: R = 0. Others take theirs, but at least B - kExponentSpan: what that flushes to zero lies below 2^-104 of
 // the first tile's scale (none where B is kLeastBase, whose rows reach down to byte 1), and no sum leaves float32's
 // range over all-zero rows (scale byte 0; 2^(15 + 80) each). With kLeastBase, factors 2^(R - B) stay in float32's
-// range for rows up to byte 207 (2^80) behind a first tile of any scale; counted from the tile's own B, ordinary rows
-// behind a tile of scale byte 1 gave NaN.
+// range for rows up to byte 187 (2^60) behind a first tile of any scale, and so do their products with the columns'
+// (scales beyond that: up to 2^100 times the first tile's); counted from the tile's own B, ordinary rows behind a tile
+// of scale byte 1 gave NaN.
 constexpr int kNoRow = 1024;  // of a row behind the last visible one: its factors come out 0
 constexpr int kExponentSpan = 80, kLeastBase = kExponentSpan + 1, kEvenBelow = 10, kEvenAbove = 12;
 // cost units by which the tile list is shared out: a tile, and the start of a group (its queries, its output)

@@ -385,8 +385,9 @@ size_t hca_shared_attend_workspace(const csa_cache *cache, int32_t n_queries, in
  *   workspace  >= hca_shared_attend_workspace(cache, n_queries, heads) bytes, 256-byte
  *              aligned: group records and two float32 partial outputs per SM
  * Scale bytes of visible blocks are finite ones (an E4M3 NaN scale would reach every
- * query of its tile). E8M0 scales reach up to 2^80, or up to 2^126 times the smallest
- * non-zero ones of the slot.
+ * query of its tile). E8M0 scales reach up to 2^60, or up to 2^100 times the smallest
+ * non-zero ones of the slot. Logits are float32 numbers: from 2^26 on in magnitude they
+ * carry no fraction, and out and lse no meaning for that query and head.
  */
 csa_status hca_shared_attend(const csa_cache *cache, const void *q, int32_t n_queries, int32_t heads,
                              const int32_t *q_offsets, const int32_t *q_pos, const float *join_out,
