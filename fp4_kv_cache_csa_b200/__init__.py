@@ -472,9 +472,10 @@ def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, joi
         raise CsaError(f"{what}: q must be [queries, heads, dim], not {list(q.shape)}")
     n, heads, D = q.shape
     at = q.get_device()
-    _expect(what, "q", q, at, torch.bfloat16, (n, heads, cache.dim))
+    batch, _, codes = cache.fp4.shape
+    _expect(what, "q", q, at, torch.bfloat16, (n, heads, 2 * codes))
     _expect_cache(what, cache, at, i32)
-    _expect(what, "q_offsets", q_offsets, at, i32, (cache.batch + 1,))
+    _expect(what, "q_offsets", q_offsets, at, i32, (batch + 1,))
     if q_pos is not None:
         _expect(what, "q_pos", q_pos, at, i32, (n,))
     if join_out is not None:
