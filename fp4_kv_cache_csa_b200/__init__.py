@@ -460,7 +460,7 @@ def hca_shared_attend_workspace(cache: Cache, n_queries: int, heads: int) -> int
 def hca_shared_attend(cache: Cache, q, q_offsets, q_pos=None, join_out=None, join_lse=None,
                       softmax_scale: Optional[float] = None, out=None, lse=None, workspace=None, stream=None):
     """Dense attention of many queries over one slot's blocks (a prompt that continuations share, a prefill
-    chunk), each tile dequantized once for 64 (query, head) columns; joined with (join_out, join_lse), the
+    chunk), each tile dequantized once for 64 // H queries; joined with (join_out, join_lse), the
     float32 result of a query's own part, as one softmax. Without q_pos every query sees all blocks of its
     slot. q [Nq, H, D] bf16; returns out [Nq, H, D] bf16, and fills lse [Nq, H] float32 if given. No gradient
     is recorded."""

@@ -4,8 +4,8 @@
 // No arithmetic: every kept block's bytes of every plane (codes, scales, indexer
 // keys, their scales) are read once and written once per destination, so the
 // call is HBM-bound: 2 x 262143 blocks of 400 bytes to two slots each take 107 us
-// (5.9 TB/s), 65521 listed blocks of 32 slots 298 us (5.65 TB/s). Small calls are
-// bound by the latency of its launches.
+// (5.9 TB/s), 65521 listed blocks of 32 slots 300 us (5.6 TB/s; in place, with its waits,
+// 440). Small calls are bound by the latency of its launches.
 //
 //   copy_check_kernel  (with long lists only) finds where each job's list ends: one
 //                      thread block per 4096 entries. Lists of up to 4096 columns

@@ -20,7 +20,9 @@
 // former are loaded before the angles are computed, so that the table of the
 // run's cosines and sines (one entry per token and pair, shared by the token's
 // heads) is built while the loads are in flight; copies have nothing to wait for
-// (both in one CTA: 210 us for 8192 x 64 x 512 bf16, apart: 175 us).
+// (both in one CTA: 210 us for 8192 x 64 x 512 bf16, apart: 175 us; in place, 64 channels
+// of each vector, 29 us against 20 of the bytes). Vectors off 16 bytes go one channel at a
+// time: 690 us, in place 81.
 #include <cuda_bf16.h>
 
 #include <type_traits>

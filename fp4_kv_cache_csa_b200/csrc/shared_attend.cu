@@ -9,8 +9,10 @@
 //
 // One tile product serves 64 columns, a column being one (query, head) of the slot: all
 // 64 heads of a query, or as many whole queries as fit (H = 16: four). A tile of
-// 128 blocks is so dequantized once per 64 columns, and no column is wasted on heads
-// that a model does not have. Group = up to 64 columns; the flat list of all groups'
+// 128 blocks is so dequantized once per 64 / H queries: with 64 heads once a query, as in
+// attend.cu, and queries of one slot then share only its blocks' way into L2. Head counts
+// that do not divide 64 leave columns empty (24 of them at 40 heads: 512 x 40 heads over
+// 16384 blocks take 1.41 ms, as 64 do). Group = up to 64 columns; the flat list of all groups'
 // tiles is cut into one range per CTA by cost, and groups that several CTAs share
 // leave unnormalised partials for shared_merge_kernel.
 //
@@ -30,7 +32,7 @@
 // Warp roles (20 warps, one CTA per SM): eight dequantize (they also bring the group's queries in), eight do the
 // softmax and the outputs, two prepare the rows' exponents and scale factors a tile ahead, one thread each issues
 // the MMAs of S^T and of O^T. At D = 512 a tile of E' takes 128 KB of shared memory, which leaves no room for a
-// second one: a part (128 channels) of the next tile is dequantized as soon as O^T has read that part of this one,
+// second one of 128 blocks (two of 64 have not been tried): a part (128 channels) of the next tile is dequantized as soon as O^T has read that part of this one,
 // and S^T follows part by part. At D = 128 three tiles fit.
 //
 // What bounds it: the chain S^T -> softmax -> O^T -> dequantization of the freed parts. Measured at D = 512, 64

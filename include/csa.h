@@ -361,7 +361,7 @@ size_t hca_shared_attend_workspace(const csa_cache *cache, int32_t n_queries, in
  * Dense attention of many queries over the blocks of one slot: a prompt shared by
  * several continuations (one slot holds it once, for all of them), or a prefill
  * chunk. As hca_decode_attend over the compressed entries, with every tile of
- * blocks dequantized once for 64 (query, head) columns, no window, bf16 output,
+ * blocks dequantized once for 64 / heads queries, no window, bf16 output,
  * and an optional second part:
  *   logit_j = softmax_scale * <q[i][h], e_j>,  lse = ln sum_j exp(logit_j),
  *   out = sum_j exp(logit_j - lse) e_j   over the visible blocks j of slot b,
