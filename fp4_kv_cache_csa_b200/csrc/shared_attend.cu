@@ -21,7 +21,7 @@
 // blocks, N = 64 columns), O^T += E'^T P' (M = 128 channels, N = 64, K = 128 blocks).
 // Operands are fp16: E'_j = e_j 2^-R_j and q' = q 2^-sQ are exact (R_j: the row's
 // largest E8M0 exponent, 7 with E4M3 scales; sQ puts each column's max |q| into
-// [2^14, 2^15)); P' = 2^(u log2 e + (R_j - B) - rho) <= 2^15, with B a common exponent, is
+// [2^14, 2^15), and what lies below 2^-31 of that is off by up to 2^-39 of it); P' = 2^(u log2 e + (R_j - B) - rho) <= 2^15, with B a common exponent, is
 // rounded to fp16's 11 bits, which leaves about 1e-4 of the output's norm, an order
 // below the bf16 rounding of the output. References rho lie 7 bits below the largest logit that
 // they were taken from, so that a weight loses bits only below 2^-21 of the largest one, and all of them
