@@ -197,7 +197,8 @@ def _expect_cache(what, c, at, int32):
     """A cache of a call whose tensors are on device number `at`: dense planes whose sizes belong together, and int32
     counts beside them (with others a kernel would read and write elsewhere)."""
     n, fp4, scale, key = c.n_blocks, c.fp4, c.scale, c.idx_key
-    if (fp4.get_device() != at or n.get_device() != at or n.dtype is not int32 or n.numel() != fp4.shape[0]
+    if (fp4.get_device() != at or n.get_device() != at or n.dtype is not int32 or n.numel() < fp4.shape[0]
+            or not n.is_contiguous()
             or scale.numel() * (16 if c.scale_fmt == CSA_SCALE_E8M0_32 else 8) != fp4.numel()  # (codes: two a byte)
             or not fp4.is_contiguous() or not scale.is_contiguous() or (key is not None and not key.is_contiguous())):
         raise CsaError(f"{what}: a cache's planes must be dense tensors [batch, capacity, row] on the call's device, with "

@@ -15,6 +15,7 @@ def cache(**kw):
 BAD = {
     "counts of 64 bits": dict(n_blocks=torch.zeros(2, dtype=torch.int64)),
     "too few counts": dict(n_blocks=torch.zeros(1, dtype=torch.int32)),
+    "every other count": dict(n_blocks=torch.zeros(4, dtype=torch.int32)[::2]),
     "a slice of larger planes": dict(fp4=torch.zeros(2, 16, 64, dtype=torch.uint8)[:, :8]),
     "scales of a slice": dict(scale=torch.zeros(2, 16, 4, dtype=torch.uint8)[:, :8]),
     "keys of a slice": dict(idx_key=torch.zeros(2, 16, 64, dtype=torch.uint8)[:, :8]),
@@ -49,3 +50,5 @@ def test_others_pass_these_checks():
     slots = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(csa.CsaError, match="CUDA device"):
         csa.csa_cache_copy(cache(), cache(status=None), slots, slots)
+    with pytest.raises(csa.CsaError, match="CUDA device"):  # the counts' first ones of a longer tensor
+        csa.csa_cache_copy(cache(n_blocks=torch.zeros(5, dtype=torch.int32)), cache(), slots, slots)
