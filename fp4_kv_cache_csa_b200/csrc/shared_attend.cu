@@ -21,7 +21,8 @@
 // blocks, N = 64 columns), O^T += E'^T P' (M = 128 channels, N = 64, K = 128 blocks).
 // Operands are fp16: E'_j = e_j 2^-R_j and q' = q 2^-sQ are exact (R_j: the row's
 // largest E8M0 exponent, 7 with E4M3 scales; sQ puts each column's max |q| into
-// [2^14, 2^15), and what lies below 2^-31 of that is off by up to 2^-39 of it); P' = 2^(u log2 e + (R_j - B) - rho) <= 2^15, with B a common exponent, is
+// [2^14, 2^15), and what lies below 2^-31 of that is off by up to 2^-39 of it);
+// P' = 2^(u log2 e + (R_j - B) - rho) <= 2^15, with B a common exponent, is
 // rounded to fp16's 11 bits, which leaves about 1e-4 of the output's norm, an order
 // below the bf16 rounding of the output. References rho lie 7 bits below the largest logit that
 // they were taken from, so that a weight loses bits only below 2^-21 of the largest one, and all of them
@@ -32,7 +33,8 @@
 // Warp roles (20 warps, one CTA per SM): eight dequantize (they also bring the group's queries in), eight do the
 // softmax and the outputs, two prepare the rows' exponents and scale factors a tile ahead, one thread each issues
 // the MMAs of S^T and of O^T. At D = 512 a tile of E' takes 128 KB of shared memory, which leaves no room for a
-// second one of 128 blocks (two of 64 have not been tried): a part (128 channels) of the next tile is dequantized as soon as O^T has read that part of this one,
+// second one of 128 blocks (two of 64 have not been tried): a part (128 channels) of the next tile is dequantized as
+// soon as O^T has read that part of this one,
 // and S^T follows part by part. At D = 128 three tiles fit.
 //
 // What bounds it: the chain S^T -> softmax -> O^T -> dequantization of the freed parts. Measured at D = 512, 64
@@ -854,7 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_attend_kernel(const __grid
                         for (int e = 0; e < 2; ++e) {
                             const int col = col0 + k + e;
                             const float f = ms->fac[col];
-                            v[e] = f == 0.f ? 0.f : o[k + e] * f * unit;  // (a NaN goes on; f * unit alone may lie below float32's range)
+                            // (a NaN goes on; f * unit alone may lie below float32's range)
+                            v[e] = f == 0.f ? 0.f : o[k + e] * f * unit;
                             if (a.join_lse && col < cols && ms->jfac[col] != 0.f)
                                 v[e] = fmaf(ms->jfac[col], jo[(size_t)(k + e) * D], v[e]);
                         }
